@@ -463,6 +463,226 @@ int flce_scale(const void* src, void* dst, int64_t count, int32_t dtype, const f
                flce_stream_t stream);
 
 /*
+ * Post-training losses on per-token log probabilities, and the optimizer step.
+ *
+ * These follow the per-token losses that flce_forward gives with FLCE_NONE
+ * (loss_i = -log p_i when z_loss_multiplier is 0) and precede flce_backward,
+ * which takes d loss / d loss_i as its grad_loss[N]. Both losses below write
+ * the loss and that gradient in one call.
+ */
+
+/* How the tokens of a batch form sequences, and which of them count.
+ * - Padded (packed = 0): `sequences` rows of `cols` tokens. Each token tensor
+ *   has its own row stride (ld_*, in elements, >= cols unless sequences <= 1);
+ *   tokens of a row are adjacent.
+ * - Packed (packed = 1): `tokens` adjacent tokens; sequence s holds tokens
+ *   cu_seqlens[s] .. cu_seqlens[s+1]-1 (device int32 [sequences + 1], not
+ *   decreasing, from 0 to `tokens`; the kernels clamp what they read, so other
+ *   values give wrong results but no access outside the tensors). Tokens
+ *   outside every sequence do not count.
+ * Tokens whose mask says no do not count: whatever the other tensors hold
+ * there (infinities, NaN) is not used, and their gradient is 0. */
+typedef enum {
+  FLCE_MASK_NONE = 0,    /* every token counts                                    */
+  FLCE_MASK_BYTES = 1,   /* uint8: a token counts where the byte is not 0         */
+  FLCE_MASK_LABELS = 2   /* int64: a token counts where it is not ignore_index    */
+} flce_mask;
+
+typedef struct {
+  int64_t sequences;         /* >= 0 and <= 2^30                                  */
+  int64_t cols;              /* padded: tokens a row, >= 0; packed: ignored       */
+  int64_t tokens;            /* packed: tokens in all, <= 2^31 - 1024; padded:
+                                ignored (sequences * cols <= 2^40)                */
+  const int32_t* cu_seqlens; /* packed: device int32 [sequences + 1], else NULL   */
+  const void* mask;          /* as mask_kind says; NULL with FLCE_MASK_NONE       */
+  int64_t ld_mask;           /* row stride of the mask, in its elements (padded)  */
+  int64_t ignore_index;      /* FLCE_MASK_LABELS                                  */
+  int32_t packed;            /* 0 or 1                                            */
+  int32_t mask_kind;         /* flce_mask                                         */
+} flce_tokens;
+
+/* Approximations of KL(policy || reference) from one sampled token, with
+ * x = ref_log_prob - log_prob. */
+typedef enum {
+  FLCE_KL_K1 = 0,   /* -x                 */
+  FLCE_KL_K2 = 1,   /* x^2 / 2            */
+  FLCE_KL_K3 = 2    /* exp(x) - x - 1     */
+} flce_kl;
+
+typedef enum {
+  FLCE_TOKEN_SUM = 0,      /* sum over the tokens that count                      */
+  FLCE_TOKEN_MEAN = 1,     /* divided by their number; NaN (0/0) if there are none,
+                              with every gradient 0, as FLCE_MEAN                 */
+  FLCE_SEQUENCE_MEAN = 3   /* mean over all sequences of each one's mean over its
+                              tokens that count (0 for a sequence with none);
+                              NaN if there are no sequences                       */
+} flce_token_reduction;
+
+/*
+ * Clipped policy loss with a KL term, and its gradient. For each token that
+ * counts, with d = log_prob - old_log_prob, r = exp(d), advantage A, and
+ * lo = log(1 - clip_low), hi = log(1 + clip_high):
+ *
+ *   pg   = max(-A r, -A exp(min(max(d, lo), hi)))
+ *   pg   = -dual_clip A          where dual_clip > 0, A < 0, d > log(dual_clip)
+ *   loss = reduction of (pg + kl_coef kl)
+ *   grad = d loss / d log_prob: from -A r where (A > 0 and d <= hi), or
+ *          (A < 0 and d >= lo, and not dual-clipped), else 0, plus kl_coef kl'
+ *
+ * (A = 0 gives pg = 0 whatever r is.) The clip is decided on d, which is the
+ * same decision as on r without the rounding of exp.
+ * log_probs, old and ref have the type `dtype`; old may be NULL (r = 1: the
+ * policy is the one that drew the tokens) and ref may be NULL when kl_coef is
+ * 0. advantages are fp32, one per sequence or (advantage_per_token) laid out
+ * as the tokens. grad is fp32 whatever dtype is, because 1 / tokens is below
+ * the range of 16 bits, and because flce_backward takes it so.
+ * With `negated`, log_probs holds -log p and grad is the gradient in that.
+ * num_tokens, num_clipped (tokens that count whose policy term has no
+ * gradient because of a clip) and kl_sum may be NULL.
+ * All sums are in fixed order: repeated calls give the same bits.
+ * Token tensors need the alignment of their element only.
+ * workspace: flce_policy_workspace_bytes, 16-byte aligned, any contents.
+ */
+typedef struct {
+  flce_tokens tokens;
+  const void* log_probs;
+  const void* old_log_probs;     /* nullable */
+  const void* ref_log_probs;     /* nullable when kl_coef == 0 */
+  const float* advantages;
+  float* loss;                   /* [1] */
+  float* grad;                   /* as the tokens; nullable: loss only */
+  int64_t* num_tokens;           /* [1], nullable */
+  int64_t* num_clipped;          /* [1], nullable */
+  float* kl_sum;                 /* [1], nullable */
+  void* workspace;
+  uint64_t ws_bytes;
+  int64_t ld_log_probs, ld_old, ld_ref, ld_advantages, ld_grad;
+  double clip_low;               /* 0 <= clip_low < 1 */
+  double clip_high;              /* >= 0 */
+  double dual_clip;              /* > 1, or 0: off */
+  double kl_coef;                /* finite */
+  int32_t dtype;                 /* flce_dtype */
+  int32_t advantage_per_token;
+  int32_t kl_estimator;          /* flce_kl */
+  int32_t reduction;             /* flce_token_reduction */
+  int32_t negated;
+  int32_t reserved;              /* 0 */
+} flce_policy_args;
+
+int flce_policy_workspace_bytes(const flce_policy_args* a, size_t* bytes);
+int flce_policy_loss(const flce_policy_args* a, flce_stream_t stream);
+
+/*
+ * Preference loss over pairs of sequences, and its gradient. The batch holds
+ * an even number of sequences: the first half are the chosen ones, and
+ * sequence i of the second half is the rejected one of pair i. With s the sum
+ * (or, with `average`, the mean) over a sequence's tokens that count of
+ * log_prob - ref_log_prob (s = 0 for a sequence with none), and
+ * z = beta (s_chosen - s_rejected) - margin, a pair's loss is
+ *
+ *   FLCE_PREF_SIGMOID  -(1 - e) log sigmoid(z) - e log sigmoid(-z), e = label_smoothing
+ *   FLCE_PREF_HINGE    max(0, 1 - z)
+ *   FLCE_PREF_IPO      (z / beta - 1 / (2 beta))^2
+ *
+ * and loss is the mean over pairs (NaN if there are none). chosen_rewards and
+ * rejected_rewards hold beta s (nullable). ref may be NULL (no reference:
+ * log_prob alone). The other conventions are flce_policy_loss's.
+ */
+typedef enum { FLCE_PREF_SIGMOID = 0, FLCE_PREF_HINGE = 1, FLCE_PREF_IPO = 2 } flce_preference;
+
+typedef struct {
+  flce_tokens tokens;
+  const void* log_probs;
+  const void* ref_log_probs;     /* nullable */
+  float* loss;                   /* [1] */
+  float* grad;                   /* as the tokens; nullable: loss and rewards only */
+  float* chosen_rewards;         /* [sequences / 2], nullable */
+  float* rejected_rewards;       /* [sequences / 2], nullable */
+  void* workspace;
+  uint64_t ws_bytes;
+  int64_t ld_log_probs, ld_ref, ld_grad;
+  double beta;                   /* finite, > 0 */
+  double label_smoothing;        /* 0 <= e <= 0.5; 0 unless FLCE_PREF_SIGMOID */
+  double margin;                 /* finite */
+  int32_t dtype;                 /* flce_dtype */
+  int32_t loss_type;             /* flce_preference */
+  int32_t average;
+  int32_t negated;
+} flce_preference_args;
+
+int flce_preference_workspace_bytes(const flce_preference_args* a, size_t* bytes);
+int flce_preference_loss(const flce_preference_args* a, flce_stream_t stream);
+
+/*
+ * AdamW over many tensors. For every element, in fp32, with t = step,
+ *
+ *   g = grad * (*grad_scale, if given)
+ *   m = beta1 m + (1 - beta1) g
+ *   v = beta2 v + (1 - beta2) g^2
+ *   p = p (1 - lr weight_decay) - lr / (1 - beta1^t) m / (sqrt(v) / sqrt(1 - beta2^t) + eps)
+ *
+ * p is the master copy where there is one (it and the parameter are written),
+ * else the parameter. Parameters have the type `dtype`; gradients
+ * `grad_dtype`, which is dtype or FLCE_F32; master copies are fp32 and go
+ * with 16-bit parameters only.
+ *
+ * state_bits = 32: m and v are fp32 (exp_avg, exp_avg_sq).
+ * state_bits = 8: exp_avg holds m and exp_avg_sq holds r = sqrt(v), one e4m3
+ * byte an element, each times the fp32 scale of its block of 256 elements of
+ * one tensor (exp_avg_scale, exp_avg_sq_scale: ceil(numel / 256) values).
+ * - The scale is the block's largest magnitude / 448 (the largest e4m3
+ *   value), or 0 if that magnitude is below 2^-100: the block is then held
+ *   as zeros. A NaN or infinity makes its block NaN.
+ * - m is rounded to nearest even. r is rounded stochastically, up with the
+ *   probability of its position between its two e4m3 neighbours: beta2 moves
+ *   v by a thousandth a step, which rounding to nearest 3 mantissa bits would
+ *   drop every time. A nonzero r never becomes 0, which under a nonzero m
+ *   would make the next steps huge. The root is held, not v, because that
+ *   halves the range of exponents.
+ * - The update itself uses the unrounded m and v.
+ * - Random bits: elements are numbered through all tensors of the call, each
+ *   tensor starting at a multiple of 256. Pair k (elements 2k, 2k + 1) has
+ *   hash x of k (all arithmetic mod 2^32, C1 = 0x9E3779B1, C2 = 0x85A308D3):
+ *     key = seed C1 + step C2; key ^= key >> 16; key *= C1;
+ *     x = (k ^ key) C1; x ^= x >> 15; x *= C2; x ^= x >> 13; x *= C1; x ^= x >> 16
+ *   The even element takes the low 16 bits b, the odd one the high 16: r /
+ *   scale is written as a fixed-exponent number whose e4m3 code is its bits
+ *   without the last 20, and 16 b + 8 is added before those are dropped.
+ *
+ * Elements are dense and in the same order in every tensor of an entry. An
+ * entry's tensors must not overlap each other's or another entry's. Pointers
+ * need the alignment of their element; 16-byte aligned ones are faster.
+ * `tensors` is a host array; the call copies it, so it may be reused at once.
+ * One kernel serves up to FLCE_ADAMW_TABLE tensors; there is no workspace.
+ */
+#define FLCE_ADAMW_TABLE 448
+
+typedef struct {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;       /* state_bits == 8, else NULL */
+  float* exp_avg_sq_scale;    /* state_bits == 8, else NULL */
+  float* master;              /* nullable; all entries or none */
+  int64_t numel;              /* >= 0 */
+} flce_adamw_tensor;
+
+typedef struct {
+  const flce_adamw_tensor* tensors;   /* host [count] */
+  const float* grad_scale;            /* device [1], nullable */
+  int64_t count;                      /* >= 0 */
+  int64_t step;                       /* t >= 1 */
+  double lr, beta1, beta2, eps, weight_decay;   /* lr, eps, weight_decay >= 0;
+                                                   0 <= beta < 1; all finite */
+  uint32_t seed;
+  int32_t dtype, grad_dtype;          /* flce_dtype */
+  int32_t state_bits;                 /* 8 or 32 */
+} flce_adamw_args;
+
+int flce_adamw(const flce_adamw_args* a, flce_stream_t stream);
+
+/*
  * Synchronises `stream`, then returns the device-detected status of the last
  * pass that used `workspace`. The status is FLCE_OK, FLCE_ERR_TARGET_RANGE,
  * FLCE_ERR_TIMEOUT or (debug build) FLCE_ERR_BOUNDS, or FLCE_ERR_CUDA if the

@@ -27,6 +27,11 @@ CHUNK_AXES = {"auto": FLCE_CHUNK_AXIS_AUTO, "rows": FLCE_CHUNK_AXIS_ROWS,
               "vocab": FLCE_CHUNK_AXIS_VOCAB}
 ACCUM_DTYPES = {"fp32": FLCE_ACCUM_FP32, "weight": FLCE_ACCUM_WEIGHT}
 REDUCTIONS = {"sum": FLCE_SUM, "mean": FLCE_MEAN, "none": FLCE_NONE}
+FLCE_MASK_NONE, FLCE_MASK_BYTES, FLCE_MASK_LABELS = 0, 1, 2
+KL_ESTIMATORS = {"k1": 0, "k2": 1, "k3": 2}
+TOKEN_REDUCTIONS = {"sum": 0, "mean": 1, "sequence_mean": 3}
+PREFERENCE_LOSSES = {"sigmoid": 0, "hinge": 1, "ipo": 2}
+ADAMW_BLOCK = 256   # elements that share a scale of the 8-bit states
 
 ERRORS = {
     0: "FLCE_OK", 1: "FLCE_ERR_INVALID_ARG", 2: "FLCE_ERR_UNSUPPORTED", 3: "FLCE_ERR_ALIGNMENT",
@@ -41,6 +46,8 @@ EXPORTS = (
     "flce_profiling_enable", "flce_profiling_read", "flce_forward_noalloc",
     "flce_forward_partial", "flce_forward_combine", "flce_chunk_logits", "flce_chunk_grads",
     "flce_chunk_weighted_mse", "flce_test_fault", "flce_workspace_regions", "flce_scale",
+    "flce_policy_workspace_bytes", "flce_policy_loss", "flce_preference_workspace_bytes",
+    "flce_preference_loss", "flce_adamw",
 )
 
 
@@ -84,6 +91,48 @@ class FlceKernelTime(ctypes.Structure):
     _fields_ = [("name", ctypes.c_char * 48), ("launches", ctypes.c_uint64),
                 ("total_ms", ctypes.c_double), ("sm_mhz", ctypes.c_double),
                 ("mma_wait_operands", ctypes.c_double), ("mma_wait_accumulator", ctypes.c_double)]
+
+
+class FlceTokens(ctypes.Structure):
+    """The tokens of a batch and which of them count (include/flce.h, flce_tokens)."""
+    _fields_ = [("sequences", ctypes.c_int64), ("cols", ctypes.c_int64), ("tokens", ctypes.c_int64),
+                ("cu_seqlens", ctypes.c_void_p), ("mask", ctypes.c_void_p),
+                ("ld_mask", ctypes.c_int64), ("ignore_index", ctypes.c_int64),
+                ("packed", ctypes.c_int32), ("mask_kind", ctypes.c_int32)]
+
+
+class FlcePolicyArgs(ctypes.Structure):
+    _fields_ = [("tokens", FlceTokens)] + [(n, ctypes.c_void_p) for n in (
+        "log_probs", "old_log_probs", "ref_log_probs", "advantages", "loss", "grad", "num_tokens",
+        "num_clipped", "kl_sum", "workspace")] + [("ws_bytes", ctypes.c_uint64)] + [
+        (n, ctypes.c_int64) for n in ("ld_log_probs", "ld_old", "ld_ref", "ld_advantages",
+                                      "ld_grad")] + [
+        (n, ctypes.c_double) for n in ("clip_low", "clip_high", "dual_clip", "kl_coef")] + [
+        (n, ctypes.c_int32) for n in ("dtype", "advantage_per_token", "kl_estimator", "reduction",
+                                      "negated", "reserved")]
+
+
+class FlcePreferenceArgs(ctypes.Structure):
+    _fields_ = [("tokens", FlceTokens)] + [(n, ctypes.c_void_p) for n in (
+        "log_probs", "ref_log_probs", "loss", "grad", "chosen_rewards", "rejected_rewards",
+        "workspace")] + [("ws_bytes", ctypes.c_uint64)] + [
+        (n, ctypes.c_int64) for n in ("ld_log_probs", "ld_ref", "ld_grad")] + [
+        (n, ctypes.c_double) for n in ("beta", "label_smoothing", "margin")] + [
+        (n, ctypes.c_int32) for n in ("dtype", "loss_type", "average", "negated")]
+
+
+class FlceAdamWTensor(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in (
+        "param", "grad", "exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale",
+        "master")] + [("numel", ctypes.c_int64)]
+
+
+class FlceAdamWArgs(ctypes.Structure):
+    _fields_ = [("tensors", ctypes.c_void_p), ("grad_scale", ctypes.c_void_p),
+                ("count", ctypes.c_int64), ("step", ctypes.c_int64)] + [
+        (n, ctypes.c_double) for n in ("lr", "beta1", "beta2", "eps", "weight_decay")] + [
+        ("seed", ctypes.c_uint32), ("dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+        ("state_bits", ctypes.c_int32)]
 
 
 class FlceError(RuntimeError):
@@ -144,6 +193,13 @@ def load() -> ctypes.CDLL:
     lib.flce_workspace_regions.restype = ctypes.c_int
     lib.flce_scale.argtypes = [vp, vp, ctypes.c_int64, ctypes.c_int32, vp, vp]
     lib.flce_scale.restype = ctypes.c_int
+    for name, args in (("policy", FlcePolicyArgs), ("preference", FlcePreferenceArgs)):
+        f = getattr(lib, f"flce_{name}_workspace_bytes")
+        f.argtypes, f.restype = [ctypes.POINTER(args), ctypes.POINTER(sz)], ctypes.c_int
+        f = getattr(lib, f"flce_{name}_loss")
+        f.argtypes, f.restype = [ctypes.POINTER(args), vp], ctypes.c_int
+    lib.flce_adamw.argtypes = [ctypes.POINTER(FlceAdamWArgs), vp]
+    lib.flce_adamw.restype = ctypes.c_int
     lib.flce_test_fault.argtypes = [ctypes.c_int32, ctypes.c_int32]
     lib.flce_test_fault.restype = ctypes.c_int
     lib.flce_check_status.argtypes = [vp, vp]
@@ -282,6 +338,32 @@ def test_fault(drop_kblock: int, wait_ms: int) -> None:
 
 def scale_raw(src: int, dst: int, count: int, dtype: int, scale: int, stream: int) -> int:
     return load().flce_scale(src, dst, count, dtype, scale, stream)
+
+
+def policy_workspace_bytes(a: FlcePolicyArgs) -> int:
+    n = ctypes.c_size_t(0)
+    check(load().flce_policy_workspace_bytes(ctypes.byref(a), ctypes.byref(n)),
+          "flce_policy_workspace_bytes")
+    return n.value
+
+
+def policy_loss_raw(a: FlcePolicyArgs, stream: int) -> int:
+    return load().flce_policy_loss(ctypes.byref(a), stream)
+
+
+def preference_workspace_bytes(a: FlcePreferenceArgs) -> int:
+    n = ctypes.c_size_t(0)
+    check(load().flce_preference_workspace_bytes(ctypes.byref(a), ctypes.byref(n)),
+          "flce_preference_workspace_bytes")
+    return n.value
+
+
+def preference_loss_raw(a: FlcePreferenceArgs, stream: int) -> int:
+    return load().flce_preference_loss(ctypes.byref(a), stream)
+
+
+def adamw_raw(a: FlceAdamWArgs, stream: int) -> int:
+    return load().flce_adamw(ctypes.byref(a), stream)
 
 
 def check_status(ws: int, stream: int) -> int:

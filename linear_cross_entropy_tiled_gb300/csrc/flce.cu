@@ -18,6 +18,7 @@
 
 #include "flce.h"
 #include "kernels.h"
+#include "post_training.h"
 #include "ptx.cuh"
 
 #ifndef FLCE_NO_NVTX
@@ -798,6 +799,19 @@ std::vector<WsRegion> workspace_regions(const flce_params* p, int pass) {
 }  // namespace
 
 void flce::note_launch() { g_launches.fetch_add(1, std::memory_order_relaxed); }
+
+int flce::require_device(int* sms) {
+  DeviceInfo d;
+  const int v = device_info(&d);
+  if (v == FLCE_OK) *sms = d.sms;
+  return v;
+}
+
+int flce::run_launch(const char* name, cudaStream_t s, cudaError_t (*f)(void*), void* ctx) {
+  return launch(name, s, [&] { return f(ctx); });
+}
+
+int flce::finish_call(const void* ws, cudaStream_t s) { return debug_finish(ws, s, FLCE_OK); }
 
 void flce::set_error_detail(const char* msg) {
   snprintf(g_detail, sizeof(g_detail), "%s", msg);

@@ -1,0 +1,251 @@
+"""AdamW over many tensors in one kernel, with states in 32 bits or in 8.
+
+``AdamW`` is the optimizer; ``adamw_plan`` is the step underneath it, on
+tensors that the caller keeps. include/flce.h (flce_adamw) gives the formula
+and the 8-bit format.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Sequence
+
+import torch
+
+from . import _lib
+from .functional import _DTYPES, _stream
+
+BLOCK = _lib.ADAMW_BLOCK
+
+
+def _dense(t: torch.Tensor) -> bool:
+    """Whether t's elements fill one stretch of memory, in whatever order of its dimensions."""
+    if t.is_contiguous():
+        return True
+    n = 1
+    for size, stride in sorted(zip(t.shape, t.stride()), key=lambda d: d[1]):
+        if size != 1:
+            if stride != n:
+                return False
+            n *= size
+    return True
+
+
+def _same_order(a: torch.Tensor, b: torch.Tensor) -> bool:
+    """Whether tensors of one shape have their elements in the same places (a dimension of 1 has no say)."""
+    return a.stride() == b.stride() or a.numel() == 0 or \
+        all(n == 1 or x == y for n, x, y in zip(a.shape, a.stride(), b.stride()))
+
+
+class _Plan:
+    """The tensors of a step, checked once. See ``adamw_plan``."""
+
+    def __init__(self, params, exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales,
+                 master_params):
+        self.params = list(params)
+        n = len(self.params)
+        lists = {"exp_avgs": exp_avgs, "exp_avg_sqs": exp_avg_sqs,
+                 "exp_avg_scales": exp_avg_scales, "exp_avg_sq_scales": exp_avg_sq_scales,
+                 "master_params": master_params}
+        self._keep = {k: None if v is None else list(v) for k, v in lists.items()}
+        for k, v in self._keep.items():
+            if v is not None and len(v) != n:
+                raise ValueError(f"{k} must have one tensor for each of the {n} parameters")
+        if n == 0:
+            self.bits, self.dtype, self.device = 32, torch.float32, None
+            return
+        p0 = self.params[0]
+        self.dtype, self.device = p0.dtype, p0.device
+        if not p0.is_cuda:
+            raise ValueError("parameters must be CUDA tensors (there is no CPU path)")
+        if self.dtype not in _DTYPES:
+            raise TypeError(f"parameters must be float32, bfloat16 or float16, got {self.dtype}")
+        self.bits = 8 if self._keep["exp_avgs"][0].dtype == torch.float8_e4m3fn else 32
+        state = torch.float8_e4m3fn if self.bits == 8 else torch.float32
+        scales = self._keep["exp_avg_scales"], self._keep["exp_avg_sq_scales"]
+        if (self.bits == 8) != (scales[0] is not None) or (scales[0] is None) != (scales[1] is None):
+            raise ValueError("scales go with 8-bit (float8_e4m3fn) states, and with those only")
+        masters = self._keep["master_params"]
+        if masters is not None and self.dtype == torch.float32:
+            raise ValueError("float32 parameters take no master copies")
+        for i, p in enumerate(self.params):
+            if p.dtype != self.dtype or p.device != self.device:
+                raise TypeError(f"parameter {i} must be {self.dtype} on {self.device}")
+            if not _dense(p):
+                raise ValueError(f"parameter {i} must be dense")
+            same = [("exp_avgs", state), ("exp_avg_sqs", state)]
+            if masters is not None:
+                same.append(("master_params", torch.float32))
+            for k, dt in same:
+                t = self._keep[k][i]
+                if t.dtype != dt or t.device != self.device:
+                    raise TypeError(f"{k}[{i}] must be {dt} on {self.device}")
+                if t.shape != p.shape or not _same_order(t, p):
+                    raise ValueError(f"{k}[{i}] must have the shape and strides of its parameter")
+            if self.bits == 8:
+                for s in scales:
+                    if s[i].dtype != torch.float32 or s[i].device != self.device or \
+                            not s[i].is_contiguous() or s[i].numel() != -(-p.numel() // BLOCK):
+                        raise ValueError(f"the scales of parameter {i} must be float32 "
+                                         f"[{-(-p.numel() // BLOCK)}] on {self.device}")
+        self.table = (_lib.FlceAdamWTensor * n)()
+        for i, p in enumerate(self.params):
+            e = self.table[i]
+            e.param, e.numel = p.data_ptr(), p.numel()
+            e.exp_avg = self._keep["exp_avgs"][i].data_ptr()
+            e.exp_avg_sq = self._keep["exp_avg_sqs"][i].data_ptr()
+            if self.bits == 8:
+                e.exp_avg_scale, e.exp_avg_sq_scale = scales[0][i].data_ptr(), scales[1][i].data_ptr()
+            if masters is not None:
+                e.master = masters[i].data_ptr()
+
+    def step(self, grads: Sequence[torch.Tensor], *, step: int, lr: float, betas=(0.9, 0.999),
+             eps: float = 1e-8, weight_decay: float = 0.01,
+             grad_scale: Optional[torch.Tensor] = None, seed: int = 0) -> None:
+        """One update with the gradients of step number ``step`` (the first is 1).
+
+        A gradient has its parameter's dtype or float32, the same for all, and
+        is multiplied by ``grad_scale``, a float32 device scalar, if given.
+        ``seed`` picks the random bits of 8-bit states, together with step.
+        """
+        n = len(self.params)
+        if len(grads) != n:
+            raise ValueError(f"{len(grads)} gradients for {n} parameters")
+        if n == 0:
+            return
+        gdt = grads[0].dtype
+        if gdt != self.dtype and gdt != torch.float32:
+            raise TypeError(f"gradients must be {self.dtype} or float32, got {gdt}")
+        keep = []
+        for i, (g, p) in enumerate(zip(grads, self.params)):
+            if g.dtype != gdt or g.device != self.device:
+                raise TypeError(f"gradient {i} must be {gdt} on {self.device}")
+            if g.shape != p.shape:
+                raise ValueError(f"gradient {i} must have the shape of its parameter")
+            if not _same_order(g, p):
+                g = torch.empty_strided(p.shape, p.stride(), dtype=gdt, device=self.device).copy_(g)
+                keep.append(g)
+            self.table[i].grad = g.data_ptr()
+        a = _lib.FlceAdamWArgs()
+        a.tensors, a.count, a.step = ctypes.addressof(self.table), n, step
+        if grad_scale is not None:
+            if grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or \
+                    grad_scale.device != self.device:
+                raise ValueError(f"grad_scale must be one float32 on {self.device}")
+            a.grad_scale = grad_scale.data_ptr()
+        a.lr, a.eps, a.weight_decay = lr, eps, weight_decay
+        a.beta1, a.beta2 = betas
+        a.seed = seed & 0xFFFFFFFF
+        a.dtype, a.grad_dtype, a.state_bits = _DTYPES[self.dtype], _DTYPES[gdt], self.bits
+        _lib.check(_lib.adamw_raw(a, _stream(self.device)), "flce_adamw")
+
+
+def adamw_plan(params: Sequence[torch.Tensor], exp_avgs: Sequence[torch.Tensor],
+               exp_avg_sqs: Sequence[torch.Tensor], *,
+               exp_avg_scales: Optional[Sequence[torch.Tensor]] = None,
+               exp_avg_sq_scales: Optional[Sequence[torch.Tensor]] = None,
+               master_params: Optional[Sequence[torch.Tensor]] = None) -> _Plan:
+    """The tensors of an AdamW step, checked once; ``plan.step(grads, step=..., lr=...)`` updates them.
+
+    All parameters share a dtype and a device, and each is dense. States have
+    the shape and strides of their parameter: float32, or float8_e4m3fn with
+    float32 scales ``[ceil(numel / 256)]`` (``exp_avg_sqs`` then holds the
+    square root of the second moment). ``master_params`` are float32 copies of
+    16-bit parameters. The plan holds the tensors and their addresses: make a
+    new one after giving one of them other storage.
+    """
+    return _Plan(params, exp_avgs, exp_avg_sqs, exp_avg_scales, exp_avg_sq_scales, master_params)
+
+
+class AdamW(torch.optim.Optimizer):
+    """AdamW with decoupled weight decay, one kernel for each group and dtype of parameters.
+
+    ``state_bits``: 32, or 8 for e4m3 states with a scale for each 256
+    elements (about 2 bytes a parameter instead of 8). ``master_weights``
+    keeps a float32 copy of 16-bit parameters, which takes the updates.
+    ``seed`` picks the random bits of 8-bit states. ``step(grad_scale=...)``
+    takes a float32 device scalar that multiplies every gradient.
+    """
+
+    def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay: float = 0.01, *, state_bits: int = 32, master_weights: bool = False,
+                 seed: int = 0):
+        if state_bits not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
+        for name, x in (("lr", lr), ("eps", eps), ("weight_decay", weight_decay)):
+            if not 0.0 <= x < float("inf"):
+                raise ValueError(f"{name} must be finite and not negative, got {x}")
+        if not all(0.0 <= b < 1.0 for b in betas):
+            raise ValueError(f"betas must be in [0, 1), got {betas}")
+        self._bits, self._master, self._seed = state_bits, bool(master_weights), int(seed)
+        self._plans: dict = {}
+        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay))
+
+    def _init_state(self, p: torch.Tensor) -> dict:
+        s = self.state[p]
+        dt = torch.float8_e4m3fn if self._bits == 8 else torch.float32
+        s["step"] = 0
+        for k in ("exp_avg", "exp_avg_sq"):
+            z = torch.empty_strided(p.shape, p.stride(), dtype=dt, device=p.device)
+            (z.view(torch.uint8) if self._bits == 8 else z).zero_()
+            s[k] = z
+            if self._bits == 8:
+                s[k + "_scale"] = torch.zeros(-(-p.numel() // BLOCK), device=p.device)
+        if self._master and p.dtype != torch.float32:
+            s["master"] = torch.empty_strided(p.shape, p.stride(), dtype=torch.float32,
+                                              device=p.device).copy_(p.detach())
+        return s
+
+    def _plan(self, params: list) -> _Plan:
+        # A plan is kept while every tensor in it keeps its place in memory.
+        states = [self.state[p] for p in params]
+        names = [k for k in ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master")
+                 if k in states[0]]
+        where = [p.data_ptr() for p in params] + [s[k].data_ptr() for s in states for k in names]
+        key = tuple(id(p) for p in params)
+        held = self._plans.get(key)
+        if held is None or held[0] != where:
+            lists = {k: [s[k] for s in states] for k in names}
+            plan = adamw_plan([p.detach() for p in params], lists["exp_avg"], lists["exp_avg_sq"],
+                              exp_avg_scales=lists.get("exp_avg_scale"),
+                              exp_avg_sq_scales=lists.get("exp_avg_sq_scale"),
+                              master_params=lists.get("master"))
+            held = self._plans[key] = (where, plan)
+        return held[1]
+
+    @torch.no_grad()
+    def step(self, closure=None, *, grad_scale: Optional[torch.Tensor] = None):
+        loss = None
+        if closure is not None:
+            with torch.enable_grad():
+                loss = closure()
+        for group in self.param_groups:
+            batches: dict = {}
+            for p in group["params"]:
+                if p.grad is None:
+                    continue
+                if p.grad.is_sparse:
+                    raise RuntimeError("AdamW does not take sparse gradients")
+                s = self.state[p]
+                if not s:
+                    s = self._init_state(p)
+                s["step"] += 1
+                batches.setdefault((p.dtype, p.device, p.grad.dtype, s["step"]), []).append(p)
+            for (_, _, _, t), params in batches.items():
+                self._plan(params).step([p.grad for p in params], step=t, lr=float(group["lr"]),
+                                        betas=group["betas"], eps=group["eps"],
+                                        weight_decay=group["weight_decay"], grad_scale=grad_scale,
+                                        seed=self._seed)
+        return loss
+
+    def load_state_dict(self, state_dict: dict) -> None:
+        """Restores the states in the types they were saved in (8 or 32 bits, whatever the parameters')."""
+        super().load_state_dict(state_dict)
+        order = [i for g in state_dict["param_groups"] for i in g["params"]]
+        params = [p for g in self.param_groups for p in g["params"]]
+        for i, p in zip(order, params):
+            saved = state_dict["state"].get(i)
+            if saved is None:
+                continue
+            self.state[p] = {k: v.detach().to(device=p.device, copy=True)
+                             if isinstance(v, torch.Tensor) else v for k, v in saved.items()}
+        self._plans.clear()

@@ -602,7 +602,7 @@ typedef struct {
   uint64_t ws_bytes;
   int64_t ld_log_probs, ld_ref, ld_grad;
   double beta;                   /* finite, > 0 */
-  double label_smoothing;        /* 0 <= e <= 0.5; 0 unless FLCE_PREF_SIGMOID */
+  double label_smoothing;        /* 0 <= e <= 0.5; FLCE_PREF_SIGMOID's alone */
   double margin;                 /* finite */
   int32_t dtype;                 /* flce_dtype */
   int32_t loss_type;             /* flce_preference */

@@ -15,11 +15,48 @@ namespace {
 
 constexpr int kBlock = 256;          // elements of a state block
 constexpr int kThreads = 256;
+// Thread blocks per SM. 8-bit states at 525M elements: 885 us with 6 (40
+// registers, a few spilled), 905 with 5, 965 with 4. 32-bit states do not mind.
+template <int kBits>
+constexpr int kPerSm = kBits == 8 ? 6 : 5;
 constexpr unsigned kC1 = 0x9E3779B1u, kC2 = 0x85A308D3u;
 
 #ifdef FLCE_DEBUG
 __device__ int g_adamw_status;
 #endif
+
+// ------------------------------------------------- 8 neighbouring elements
+// Each type's vector load and store of 8 elements: 32 bytes of fp32 (one
+// 256-bit access), 16 of a 16-bit type, 8 of e4m3. Nothing is read twice, so
+// the loads leave L1 alone.
+__device__ __forceinline__ void load8(const float* p, float (&x)[8]) {
+  asm volatile("ld.global.L1::no_allocate.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]),
+                 "=f"(x[6]), "=f"(x[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void store8(float* p, const float (&x)[8]) {
+  asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(x[0]),
+               "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7])
+               : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
+  uint32_t w[4];
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "l"(p));
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    x[2 * k] = Elem<T>::lo(w[k]);
+    x[2 * k + 1] = Elem<T>::hi(w[k]);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T* p, const float (&x)[8]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(Elem<T>::pack(x[0], x[1]), Elem<T>::pack(x[2], x[3]),
+                                            Elem<T>::pack(x[4], x[5]), Elem<T>::pack(x[6], x[7]));
+}
 
 __device__ __forceinline__ float to_f32(float x) { return x; }
 __device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -31,19 +68,82 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
 }
 template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
 
-__device__ __forceinline__ float e4m3_to_f32(unsigned char b) {
-  return __half2float(__half(__nv_cvt_fp8_to_halfraw(b, __NV_E4M3)));
+// The same element by element, for tensors off their alignment and for a
+// tensor's last block: `n` elements count, the others read as 0.
+template <typename T>
+__device__ __forceinline__ void load_some(const T* p, int n, float (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = k < n ? to_f32(p[k]) : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ void store_some(T* p, int n, const float (&x)[8]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < n) p[k] = from_f32<T>(x[k]);
 }
 
-// Larger of two magnitudes, NaN if either is.
+template <bool kVec, typename T>
+__device__ __forceinline__ void load(const T* p, int n, float (&x)[8]) {
+  if (kVec) load8(p, x); else load_some(p, n, x);
+}
+// `r`: the tensor the store must stay in (checked in FLCE_DEBUG builds).
+template <bool kVec, typename T>
+__device__ __forceinline__ void store(T* p, int n, const float (&x)[8], const DevRegion& r, int* status) {
+  if (n <= 0 || !store_allowed(p, (n < 8 ? n : 8) * sizeof(T), r, status)) return;
+  if (kVec) store8(p, x); else store_some(p, n, x);
+}
+
+// ------------------------------------------------------- 8-bit state format
+__device__ __forceinline__ void e4m3_to_f32(uint2 w, float (&x)[8]) {
+  const uint32_t v[2] = {w.x, w.y};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        static_cast<__nv_fp8x2_storage_t>(v[k / 2] >> (16 * (k & 1))), __NV_E4M3);
+    const float2 f = __half22float2(__half2(h));
+    x[2 * k] = f.x;
+    x[2 * k + 1] = f.y;
+  }
+}
+template <bool kVec>
+__device__ __forceinline__ uint2 load_codes(const unsigned char* p, int n) {
+  uint2 w = make_uint2(0u, 0u);
+  if (kVec) {
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(w.x), "=r"(w.y) : "l"(p));
+    return w;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < n) (k < 4 ? w.x : w.y) |= static_cast<uint32_t>(p[k]) << (8 * (k & 3));
+  return w;
+}
+template <bool kVec>
+__device__ __forceinline__ void store_codes(unsigned char* p, int n, uint2 w, const DevRegion& r,
+                                            int* status) {
+  if (n <= 0 || !store_allowed(p, n < 8 ? n : 8, r, status)) return;
+  if (kVec) {
+    *reinterpret_cast<uint2*>(p) = w;
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (k < n) p[k] = static_cast<unsigned char>((k < 4 ? w.x : w.y) >> (8 * (k & 3)));
+}
+
+// Largest magnitude of the warp's values, NaN if one is NaN.
+__device__ __forceinline__ float warp_max_nan(float v) {
+  float r;
+  asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
+}
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
   return r;
 }
 
-__device__ __forceinline__ unsigned pair_hash(unsigned pair, unsigned key) {
-  unsigned x = (pair ^ key) * kC1;
+__device__ __forceinline__ unsigned pair_hash(unsigned x) {
+  x *= kC1;
   x ^= x >> 15;
   x *= kC2;
   x ^= x >> 13;
@@ -51,118 +151,238 @@ __device__ __forceinline__ unsigned pair_hash(unsigned pair, unsigned key) {
   return x ^ (x >> 16);
 }
 
-// r x 448 / (largest) in [0, 448], or NaN -> e4m3 byte with the 16 random
-// bits. x 2^-120 has e4m3's exponent field where fp32 has its own (bias 7
-// against 127, subnormals included), so the code is its bits without the last
-// 20, and adding random bits below them rounds up with the right probability.
-__device__ __forceinline__ unsigned char e4m3_stochastic(float x, unsigned random16) {
-  if (isnan(x)) return 0x7F;
-  unsigned code = (__float_as_uint(x * 0x1p-120f) + (random16 << 4) + 8u) >> 20;
-  code = code > 0x7Eu ? 0x7Eu : code;
-  return static_cast<unsigned char>(x > 0.f && code == 0u ? 1u : code);
+// Square roots of 8 second moments. With y = 1/sqrt(v) approximated, s = v y
+// is off by a unit or two in the last place, and one Newton step on its exact
+// residual v - s^2 leaves the root rounded to nearest, all but surely. That is
+// half the instructions of eight sqrtf, which take over (for the warp) where a
+// value is 0, so small that its residual would underflow, infinite or NaN.
+__device__ __forceinline__ void roots(const float (&v)[8], float lo, float (&r)[8]) {
+  float hi = v[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) hi = max_nan(hi, v[k]);
+  if (__any_sync(0xffffffffu, !(lo >= 0x1p-80f && hi < INFINITY))) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = sqrtf(v[k]);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; k += 2) {
+    float y0, y1;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y0) : "f"(v[k]));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y1) : "f"(v[k + 1]));
+    const unsigned long long y = f2pack(y0, y1), vv = f2pack(v[k], v[k + 1]);
+    const unsigned long long s = mul2(vv, y), h = mul2(y, f2pack(-0.5f, -0.5f));
+    f2unpack(fma2(fma2(s, s, f2pack(-v[k], -v[k + 1])), h, s), r[k], r[k + 1]);
+  }
 }
 
-template <typename P, typename G, int kBits>
-__global__ void __launch_bounds__(kThreads) adamw_kernel(const __grid_constant__ AdamWArgs a) {
+// A tensor of the table, with what the blocks of it have in common.
+struct Entry {
+  void* param;
+  const void* grad;
+  void* exp_avg;
+  void* exp_avg_sq;
+  float* exp_avg_scale;
+  float* exp_avg_sq_scale;
+  float* master;
+  long long numel;
+};
+
+// One state block of 256 elements, 8 a lane.
+template <typename P, typename G, int kBits, bool kMaster, bool kVec>
+__device__ __forceinline__ void step_block(const AdamWArgs& a, const Entry& t, unsigned sb,
+                                           unsigned pair0, float gs) {
   const int lane = threadIdx.x & 31;
-  const unsigned gb = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);   // of this launch
-  if (gb >= a.block0[a.count]) return;
-  int lo = 0, hi = a.count;   // the last tensor that starts at or before gb
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.block0[mid] <= gb) lo = mid; else hi = mid;
-  }
-  const flce_adamw_tensor& t = a.t[lo];
-  const unsigned sb = gb - a.block0[lo];
   const long long e0 = static_cast<long long>(sb) * kBlock + lane * 8;
-  const float gs = a.grad_scale != nullptr ? *a.grad_scale : 1.f;
-  P* p = static_cast<P*>(t.param);
-  const G* g = static_cast<const G*>(t.grad);
-  float ms = 0.f, vs = 0.f, m[8], r[8];
+  const long long rest = t.numel - e0;
+  const int n = kVec || rest > 8 ? 8 : static_cast<int>(rest);   // of this lane's 8
+  P* const p = static_cast<P*>(t.param) + e0;
+  float g[8], m[8], v[8], x[8];
+  load<kVec>(static_cast<const G*>(t.grad) + e0, n, g);
   if (kBits == 8) {
-    ms = t.exp_avg_scale[sb];
-    vs = t.exp_avg_sq_scale[sb];
+    const uint2 cm = load_codes<kVec>(static_cast<const unsigned char*>(t.exp_avg) + e0, n);
+    const uint2 cv = load_codes<kVec>(static_cast<const unsigned char*>(t.exp_avg_sq) + e0, n);
+    const float ms = t.exp_avg_scale[sb], vs = t.exp_avg_sq_scale[sb];
+    if (kMaster) load<kVec>(t.master + e0, n, x); else load<kVec>(p, n, x);
+    e4m3_to_f32(cm, m);
+    e4m3_to_f32(cv, v);
+    mul_pairs(m, m, ms);
+    mul_pairs(v, v, vs);
+    mul_pairs(v, v, v);
+  } else {
+    load<kVec>(static_cast<const float*>(t.exp_avg) + e0, n, m);
+    load<kVec>(static_cast<const float*>(t.exp_avg_sq) + e0, n, v);
+    if (kMaster) load<kVec>(t.master + e0, n, x); else load<kVec>(p, n, x);
   }
-  float top_m = 0.f, top_r = 0.f;
+  // Each product and sum is rounded by itself: an 8-bit state is then the same
+  // on every implementation of the formula, where one last bit could pick
+  // another code. (The sums stay out of packed arithmetic, which would fuse
+  // them with the products.)
+  float mg[8], vg[8], root[8];
+  mul_pairs(g, g, gs);
+  mul_pairs(mg, g, a.one_beta1);
+  mul_pairs(vg, g, g);
+  mul_pairs(vg, vg, a.one_beta2);
+  mul_pairs(m, m, a.beta1);
+  mul_pairs(v, v, a.beta2);
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    m[k] = 0.f;
-    r[k] = 0.f;
-    const long long i = e0 + k;
-    if (i >= t.numel) continue;
-    float mm, v;
-    if (kBits == 8) {
-      mm = e4m3_to_f32(static_cast<const unsigned char*>(t.exp_avg)[i]) * ms;
-      v = e4m3_to_f32(static_cast<const unsigned char*>(t.exp_avg_sq)[i]) * vs;
-      v *= v;
-    } else {
-      mm = static_cast<const float*>(t.exp_avg)[i];
-      v = static_cast<const float*>(t.exp_avg_sq)[i];
-    }
-    const float gr = to_f32(g[i]) * gs;
-    // rounded product by product, not fused: an 8-bit state is then the same on every
-    // implementation of the formula, where one last bit could pick another code
-    mm = __fadd_rn(__fmul_rn(a.beta1, mm), __fmul_rn(a.one_beta1, gr));
-    v = __fadd_rn(__fmul_rn(a.beta2, v), __fmul_rn(a.one_beta2, __fmul_rn(gr, gr)));
-    const float root = sqrtf(v);
-    float x = t.master != nullptr ? t.master[i] : to_f32(p[i]);
-    x = x * a.decay - a.step_size * mm / (root * a.inv_root_bc2 + a.eps);
-    if (t.master != nullptr) t.master[i] = x;
-    if (store_allowed(p + i, sizeof(P), DevRegion{p, t.numel * sizeof(P)}, a.status)) p[i] = from_f32<P>(x);
-    if (kBits == 32) {
-      static_cast<float*>(t.exp_avg)[i] = mm;
-      static_cast<float*>(t.exp_avg_sq)[i] = v;
-    } else {
-      m[k] = mm;
-      r[k] = root;
-      top_m = max_nan(top_m, fabsf(mm));
-      top_r = max_nan(top_r, root);
-    }
+    m[k] = __fadd_rn(m[k], mg[k]);
+    v[k] = __fadd_rn(v[k], vg[k]);
   }
-  if (kBits == 32) return;
+  float lo = v[0];
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) {
-    top_m = max_nan(top_m, __shfl_xor_sync(0xffffffffu, top_m, o));
-    top_r = max_nan(top_r, __shfl_xor_sync(0xffffffffu, top_r, o));
-  }
-  // !(x < y): a NaN takes the first branch and makes the block NaN
-  const float im = !(top_m < 0x1p-100f) ? 448.f / top_m : 0.f;
-  const float ir = !(top_r < 0x1p-100f) ? 448.f / top_r : 0.f;
-  if (lane == 0) {
-    t.exp_avg_scale[sb] = !(top_m < 0x1p-100f) ? top_m / 448.f : 0.f;
-    t.exp_avg_sq_scale[sb] = !(top_r < 0x1p-100f) ? top_r / 448.f : 0.f;
-  }
-  const unsigned pair0 = (a.first_block + gb) * (kBlock / 2) + lane * 4;   // mod 2^32
+  for (int k = 1; k < 8; ++k) lo = fminf(lo, v[k]);
+  roots(v, lo, root);
+  float q[8], den[8];
+  mul_pairs(q, m, -a.step_size);
+  fma_pairs(den, root, a.inv_root_bc2, a.eps);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const long long i = e0 + k;
-    if (i >= t.numel) continue;
-    const unsigned x = pair_hash(pair0 + k / 2, a.key);
-    static_cast<unsigned char*>(t.exp_avg)[i] = __nv_cvt_float_to_fp8(m[k] * im, __NV_SATFINITE, __NV_E4M3);
-    static_cast<unsigned char*>(t.exp_avg_sq)[i] = e4m3_stochastic(r[k] * ir, k & 1 ? x >> 16 : x & 0xffffu);
+  for (int k = 0; k < 8; ++k) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(den[k]) : "f"(den[k]));
+  mul_pairs(q, q, den);
+  fma_pairs(x, x, a.decay, q);
+  const long long numel = t.numel;
+  if (kMaster)
+    store<kVec>(t.master + e0, n, x, DevRegion{t.master, numel * 4ull}, a.status);
+  store<kVec>(p, n, x, DevRegion{t.param, numel * sizeof(P)}, a.status);
+  if (kBits == 32) {
+    store<kVec>(static_cast<float*>(t.exp_avg) + e0, n, m, DevRegion{t.exp_avg, numel * 4ull}, a.status);
+    store<kVec>(static_cast<float*>(t.exp_avg_sq) + e0, n, v, DevRegion{t.exp_avg_sq, numel * 4ull},
+                a.status);
+    return;
+  }
+  float top_m = fabsf(m[0]), top_r = root[0];
+#pragma unroll
+  for (int k = 1; k < 8; ++k) {
+    top_m = max_nan(top_m, fabsf(m[k]));
+    top_r = max_nan(top_r, root[k]);
+  }
+  top_m = warp_max_nan(top_m);
+  top_r = warp_max_nan(top_r);
+  // !(x < y) holds for a NaN; a block with an infinity or NaN becomes NaN
+  const bool has_m = !(top_m < 0x1p-100f), has_r = !(top_r < 0x1p-100f);
+  const float im = top_m < INFINITY ? (has_m ? __fmul_rn(__frcp_rn(top_m), 448.f) : 0.f) : NAN;
+  const float ir = has_r ? __fmul_rn(__frcp_rn(top_r), 448.f) : 0.f;
+  const DevRegion r_ms{t.exp_avg_scale, (numel + 255) / 256 * 4ull};
+  const DevRegion r_vs{t.exp_avg_sq_scale, (numel + 255) / 256 * 4ull};
+  if (lane == 0 && store_allowed(t.exp_avg_scale + sb, 4, r_ms, a.status) &&
+      store_allowed(t.exp_avg_sq_scale + sb, 4, r_vs, a.status)) {
+    t.exp_avg_scale[sb] = has_m ? top_m * (1.f / 448.f) : 0.f;
+    t.exp_avg_sq_scale[sb] = has_r ? top_r * (1.f / 448.f) : 0.f;
+  }
+  // m to nearest. The root y = root / scale is in [0, 448]: y 2^-120 has
+  // e4m3's exponent field where fp32 has its own (bias 7 against 127,
+  // subnormals included), so its code is those bits without the last 20, and
+  // 16 random bits added right below the code round it up with the probability
+  // of its place between two codes. All of it 4 bits up, so that the code is
+  // the top byte (y = 448 lies 7 units from a carry out of it).
+  mul_pairs(m, m, im);
+  float y[8];
+  mul_pairs(y, root, ir);
+  uint32_t cm[4], cv[8];
+  const unsigned pair = (pair0 + lane * 4) ^ a.key;   // a multiple of 4 before the key
+  // Where every root of the warp is above e4m3's smallest normal value, 2^-6
+  // (with 1 % to spare for the roundings), 2^-120 comes off the exponent field
+  // as a constant in the byte above the random ones, and no code can be 0.
+  const float normal = top_r * (1.01f * 0x1p-6f / 448.f);
+  if (!__any_sync(0xffffffffu, !(lo > normal * normal))) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const unsigned h = pair_hash(pair ^ (k / 2));
+      cv[k] = (__float_as_uint(y[k]) << 4) + __byte_perm(h, 0x40000080u, k & 1 ? 0x7324 : 0x7104);
+    }
+  } else {
+    mul_pairs(y, y, 0x1p-120f);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      // A root that is not 0 is at least 2^-75, so its bits are above 1 << 24: code 1 at least.
+      const unsigned floor1 = has_r ? min(__float_as_uint(root[k]), 1u << 24) : 0u;
+      const unsigned h = pair_hash(pair ^ (k / 2));
+      cv[k] = max((__float_as_uint(y[k]) << 4) + __byte_perm(h, 0x80u, k & 1 ? 0x5324 : 0x5104), floor1);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    cm[k] = __nv_cvt_float2_to_fp8x2(make_float2(m[2 * k], m[2 * k + 1]), __NV_SATFINITE, __NV_E4M3);
+  uint2 wm = make_uint2(__byte_perm(cm[0], cm[1], 0x5410), __byte_perm(cm[2], cm[3], 0x5410));
+  uint2 wv = make_uint2(__byte_perm(__byte_perm(cv[0], cv[1], 0x0073), __byte_perm(cv[2], cv[3], 0x0073), 0x5410),
+                        __byte_perm(__byte_perm(cv[4], cv[5], 0x0073), __byte_perm(cv[6], cv[7], 0x0073), 0x5410));
+  if (!(top_r < INFINITY)) wv = make_uint2(0x7F7F7F7Fu, 0x7F7F7F7Fu);
+  store_codes<kVec>(static_cast<unsigned char*>(t.exp_avg) + e0, n, wm,
+                    DevRegion{t.exp_avg, static_cast<unsigned long long>(numel)}, a.status);
+  store_codes<kVec>(static_cast<unsigned char*>(t.exp_avg_sq) + e0, n, wv,
+                    DevRegion{t.exp_avg_sq, static_cast<unsigned long long>(numel)}, a.status);
+}
+
+// The tensor of block gb: the last one that starts at or before it. The warp
+// looks at every 16th start, then at the 16 from there: two reads of the
+// constant bank one after the other, where bisection takes up to nine.
+__device__ __forceinline__ int tensor_of(const AdamWArgs& a, unsigned gb) {
+  static_assert(FLCE_ADAMW_TABLE <= 512, "32 steps of 16");
+  const int lane = threadIdx.x & 31;
+  int i = lane * 16;
+  const int from = 16 * (__popc(__ballot_sync(0xffffffffu, i < a.count && a.block0[i] <= gb)) - 1);
+  i = from + lane;
+  return from - 1 + __popc(__ballot_sync(0xffffffffu, lane < 16 && i < a.count && a.block0[i] <= gb));
+}
+
+template <typename P, typename G, int kBits, bool kMaster>
+__global__ void __launch_bounds__(kThreads, kPerSm<kBits>) adamw_kernel(const __grid_constant__ AdamWArgs a) {
+  const unsigned warps = gridDim.x * (kThreads / 32);
+  // of this launch; the shuffle tells the compiler that it is the same in the warp
+  unsigned gb = __shfl_sync(0xffffffffu, blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), 0);
+  const unsigned total = a.block0[a.count];
+  if (gb >= total) return;
+  const float gs = a.grad_scale != nullptr ? *a.grad_scale : 1.f;
+  while (true) {
+    const int lo = tensor_of(a, gb);
+    const flce_adamw_tensor& e = a.t[lo];
+    const Entry t{e.param, e.grad, e.exp_avg, e.exp_avg_sq, e.exp_avg_scale, e.exp_avg_sq_scale,
+                  e.master, e.numel};
+    const uintptr_t all = reinterpret_cast<uintptr_t>(t.param) | reinterpret_cast<uintptr_t>(t.grad) |
+                          reinterpret_cast<uintptr_t>(t.exp_avg) |
+                          reinterpret_cast<uintptr_t>(t.exp_avg_sq) |
+                          reinterpret_cast<uintptr_t>(t.master);
+    const unsigned first = a.block0[lo], end = a.block0[lo + 1];
+    const unsigned full = (all & 31u) == 0 ? first + static_cast<unsigned>(t.numel / kBlock) : first;
+    for (; gb < end; gb += warps) {
+      const unsigned pair0 = (a.first_block + gb) * (kBlock / 2);   // mod 2^32
+      if (gb < full)
+        step_block<P, G, kBits, kMaster, true>(a, t, gb - first, pair0, gs);
+      else
+        step_block<P, G, kBits, kMaster, false>(a, t, gb - first, pair0, gs);
+    }
+    if (gb >= total) return;
   }
 }
 
-template <typename P, typename G>
-cudaError_t launch_bits(const AdamWArgs& a, int bits, unsigned grid, cudaStream_t s) {
-  if (bits == 8)
-    adamw_kernel<P, G, 8><<<grid, kThreads, 0, s>>>(a);
-  else
-    adamw_kernel<P, G, 32><<<grid, kThreads, 0, s>>>(a);
+template <typename P, typename G, int kBits, bool kMaster>
+cudaError_t launch_kernel(const AdamWArgs& a, int sms, cudaStream_t s) {
+  const unsigned need = (a.block0[a.count] + kThreads / 32 - 1) / (kThreads / 32);
+  const unsigned most = static_cast<unsigned>(sms) * kPerSm<kBits>;
+  adamw_kernel<P, G, kBits, kMaster><<<need < most ? need : most, kThreads, 0, s>>>(a);
   note_launch();
   return cudaGetLastError();
 }
 
+template <typename P, typename G>
+cudaError_t launch_types(const AdamWArgs& a, int bits, int sms, cudaStream_t s) {
+  if constexpr (sizeof(P) == 2)
+    if (a.t[0].master != nullptr)
+      return bits == 8 ? launch_kernel<P, G, 8, true>(a, sms, s) : launch_kernel<P, G, 32, true>(a, sms, s);
+  return bits == 8 ? launch_kernel<P, G, 8, false>(a, sms, s) : launch_kernel<P, G, 32, false>(a, sms, s);
+}
+
 }  // namespace
 
-cudaError_t launch_adamw(const AdamWArgs& a, int dtype, int grad_dtype, int bits, cudaStream_t s) {
-  const unsigned grid = (a.block0[a.count] + kThreads / 32 - 1) / (kThreads / 32);
-  if (dtype == FLCE_F32) return launch_bits<float, float>(a, bits, grid, s);
+cudaError_t launch_adamw(const AdamWArgs& a, int dtype, int grad_dtype, int bits, int sms,
+                         cudaStream_t s) {
+  if (dtype == FLCE_F32) return launch_types<float, float>(a, bits, sms, s);
   if (dtype == FLCE_BF16)
-    return grad_dtype == FLCE_F32 ? launch_bits<__nv_bfloat16, float>(a, bits, grid, s)
-                                  : launch_bits<__nv_bfloat16, __nv_bfloat16>(a, bits, grid, s);
-  return grad_dtype == FLCE_F32 ? launch_bits<__half, float>(a, bits, grid, s)
-                                : launch_bits<__half, __half>(a, bits, grid, s);
+    return grad_dtype == FLCE_F32 ? launch_types<__nv_bfloat16, float>(a, bits, sms, s)
+                                  : launch_types<__nv_bfloat16, __nv_bfloat16>(a, bits, sms, s);
+  return grad_dtype == FLCE_F32 ? launch_types<__half, float>(a, bits, sms, s)
+                                : launch_types<__half, __half>(a, bits, sms, s);
 }
 
 cudaError_t adamw_status(int** status) {

@@ -130,8 +130,7 @@ int check_preference(const flce_preference_args* a) {
     return refuse(FLCE_ERR_INVALID_ARG, "loss_type");
   if (!std::isfinite(a->beta) || a->beta <= 0.0) return refuse(FLCE_ERR_INVALID_ARG, "beta");
   if (!std::isfinite(a->margin)) return refuse(FLCE_ERR_INVALID_ARG, "margin");
-  if (!(a->label_smoothing >= 0.0 && a->label_smoothing <= 0.5) ||
-      (a->label_smoothing != 0.0 && a->loss_type != FLCE_PREF_SIGMOID))
+  if (!(a->label_smoothing >= 0.0 && a->label_smoothing <= 0.5))
     return refuse(FLCE_ERR_INVALID_ARG, "label_smoothing");
   if ((a->average & ~1) != 0 || (a->negated & ~1) != 0)
     return refuse(FLCE_ERR_INVALID_ARG, "average or negated");
@@ -330,6 +329,7 @@ int flce_adamw(const flce_adamw_args* a, flce_stream_t stream) {
   if (!aligned(a->grad_scale, 4)) return refuse(FLCE_ERR_ALIGNMENT, "grad_scale");
   const size_t pe = elem_bytes(a->dtype), ge = elem_bytes(a->grad_dtype);
   const size_t se = a->state_bits == 8 ? 1 : 4;
+  const flce_adamw_tensor* first = nullptr;
   for (int64_t i = 0; i < a->count; ++i) {
     const flce_adamw_tensor& t = a->tensors[i];
     if (t.numel < 0 || t.numel > (int64_t(1) << 38)) return refuse(FLCE_ERR_INVALID_ARG, "numel");
@@ -343,8 +343,11 @@ int flce_adamw(const flce_adamw_args* a, flce_stream_t stream) {
       return refuse(FLCE_ERR_INVALID_ARG, "scales with 32-bit states");
     if (t.master != nullptr && a->dtype == FLCE_F32)
       return refuse(FLCE_ERR_INVALID_ARG, "a master copy of fp32 parameters");
-    if ((t.master != nullptr) != (a->tensors[0].master != nullptr) && t.numel > 0)
-      return refuse(FLCE_ERR_INVALID_ARG, "master copies of some tensors only");
+    if (t.numel > 0) {   // an empty tensor may have any pointers
+      if (first == nullptr) first = &t;
+      if ((t.master != nullptr) != (first->master != nullptr))
+        return refuse(FLCE_ERR_INVALID_ARG, "master copies of some tensors only");
+    }
     if (!aligned(t.param, pe) || !aligned(t.grad, ge) || !aligned(t.exp_avg, se) ||
         !aligned(t.exp_avg_sq, se) || !aligned(t.exp_avg_scale, 4) ||
         !aligned(t.exp_avg_sq_scale, 4) || !aligned(t.master, 4))
@@ -392,7 +395,7 @@ int flce_adamw(const flce_adamw_args* a, flce_stream_t stream) {
     if (k.count == 0) break;
     first_block += static_cast<unsigned>(blocks);
     v = run_kernel("flce_adamw", st,
-                   [&] { return launch_adamw(k, a->dtype, a->grad_dtype, a->state_bits, st); });
+                   [&] { return launch_adamw(k, a->dtype, a->grad_dtype, a->state_bits, sms, st); });
     if (v != FLCE_OK) return v;
   }
   return finish_call(k.status, st);

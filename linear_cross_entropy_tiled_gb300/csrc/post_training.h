@@ -99,7 +99,8 @@ struct AdamWArgs {
 };
 
 // dtype and grad_dtype: flce_dtype; bits: 8 or 32.
-cudaError_t launch_adamw(const AdamWArgs& a, int dtype, int grad_dtype, int bits, cudaStream_t s);
+cudaError_t launch_adamw(const AdamWArgs& a, int dtype, int grad_dtype, int bits, int sms,
+                         cudaStream_t s);
 cudaError_t adamw_status(int** status);   // debug builds: a device word for the bounds check
 
 }  // namespace flce

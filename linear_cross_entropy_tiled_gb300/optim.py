@@ -6,15 +6,20 @@ and the 8-bit format.
 """
 from __future__ import annotations
 
-import ctypes
+from operator import attrgetter
 from typing import Optional, Sequence
 
+import numpy as np
 import torch
 
 from . import _lib
 from .functional import _DTYPES, _stream
 
 BLOCK = _lib.ADAMW_BLOCK
+
+_dtype_of, _shape_of = attrgetter("dtype"), attrgetter("shape")
+_device_of, _address_of = torch.Tensor.get_device, torch.Tensor.data_ptr
+_is_contiguous = torch.Tensor.is_contiguous
 
 
 def _dense(t: torch.Tensor) -> bool:
@@ -87,16 +92,21 @@ class _Plan:
                             not s[i].is_contiguous() or s[i].numel() != -(-p.numel() // BLOCK):
                         raise ValueError(f"the scales of parameter {i} must be float32 "
                                          f"[{-(-p.numel() // BLOCK)}] on {self.device}")
-        self.table = (_lib.FlceAdamWTensor * n)()
-        for i, p in enumerate(self.params):
-            e = self.table[i]
-            e.param, e.numel = p.data_ptr(), p.numel()
-            e.exp_avg = self._keep["exp_avgs"][i].data_ptr()
-            e.exp_avg_sq = self._keep["exp_avg_sqs"][i].data_ptr()
-            if self.bits == 8:
-                e.exp_avg_scale, e.exp_avg_sq_scale = scales[0][i].data_ptr(), scales[1][i].data_ptr()
-            if masters is not None:
-                e.master = masters[i].data_ptr()
+        # the host table of flce_adamw: one row of eight words a tensor
+        self.table = np.zeros((n, 8), dtype=np.uint64)
+        for k, name in ((2, "exp_avgs"), (3, "exp_avg_sqs"), (4, "exp_avg_scales"),
+                        (5, "exp_avg_sq_scales"), (6, "master_params")):
+            if self._keep[name] is not None:
+                self.table[:, k] = [t.data_ptr() for t in self._keep[name]]
+        self.table[:, 0] = [p.data_ptr() for p in self.params]
+        self.table[:, 7] = [p.numel() for p in self.params]
+        # what a gradient has to agree with
+        self._shapes = [p.shape for p in self.params]
+        self._contiguous = all(p.is_contiguous() for p in self.params)
+        self._index = self.device.index
+        self.args = _lib.FlceAdamWArgs()
+        self.args.tensors, self.args.count = self.table.ctypes.data, n
+        self.args.dtype, self.args.state_bits = _DTYPES[self.dtype], self.bits
 
     def step(self, grads: Sequence[torch.Tensor], *, step: int, lr: float, betas=(0.9, 0.999),
              eps: float = 1e-8, weight_decay: float = 0.01,
@@ -115,27 +125,27 @@ class _Plan:
         gdt = grads[0].dtype
         if gdt != self.dtype and gdt != torch.float32:
             raise TypeError(f"gradients must be {self.dtype} or float32, got {gdt}")
-        keep = []
-        for i, (g, p) in enumerate(zip(grads, self.params)):
-            if g.dtype != gdt or g.device != self.device:
-                raise TypeError(f"gradient {i} must be {gdt} on {self.device}")
-            if g.shape != p.shape:
-                raise ValueError(f"gradient {i} must have the shape of its parameter")
-            if not _same_order(g, p):
-                g = torch.empty_strided(p.shape, p.stride(), dtype=gdt, device=self.device).copy_(g)
-                keep.append(g)
-            self.table[i].grad = g.data_ptr()
-        a = _lib.FlceAdamWArgs()
-        a.tensors, a.count, a.step = ctypes.addressof(self.table), n, step
-        if grad_scale is not None:
+        if set(map(_dtype_of, grads)) != {gdt} or set(map(_device_of, grads)) != {self._index}:
+            raise TypeError(f"every gradient must be {gdt} on {self.device}")
+        if list(map(_shape_of, grads)) != self._shapes:
+            raise ValueError("every gradient must have the shape of its parameter")
+        if not (self._contiguous and all(map(_is_contiguous, grads))):
+            # `grads` then holds the copies until the kernel is launched
+            grads = [g if _same_order(g, p) else
+                     torch.empty_strided(p.shape, p.stride(), dtype=gdt, device=self.device).copy_(g)
+                     for g, p in zip(grads, self.params)]
+        self.table[:, 1] = list(map(_address_of, grads))
+        a = self.args
+        if grad_scale is None:
+            a.grad_scale = None
+        else:
             if grad_scale.dtype != torch.float32 or grad_scale.numel() != 1 or \
                     grad_scale.device != self.device:
                 raise ValueError(f"grad_scale must be one float32 on {self.device}")
             a.grad_scale = grad_scale.data_ptr()
-        a.lr, a.eps, a.weight_decay = lr, eps, weight_decay
+        a.step, a.lr, a.eps, a.weight_decay = step, lr, eps, weight_decay
         a.beta1, a.beta2 = betas
-        a.seed = seed & 0xFFFFFFFF
-        a.dtype, a.grad_dtype, a.state_bits = _DTYPES[self.dtype], _DTYPES[gdt], self.bits
+        a.seed, a.grad_dtype = seed & 0xFFFFFFFF, _DTYPES[gdt]
         _lib.check(_lib.adamw_raw(a, _stream(self.device)), "flce_adamw")
 
 

@@ -21,10 +21,6 @@ template <int kBits>
 constexpr int kPerSm = kBits == 8 ? 6 : 5;
 constexpr unsigned kC1 = 0x9E3779B1u, kC2 = 0x85A308D3u;
 
-#ifdef FLCE_DEBUG
-__device__ int g_adamw_status;
-#endif
-
 // ------------------------------------------------- 8 neighbouring elements
 // Each type's vector load and store of 8 elements: 32 bytes of fp32 (one
 // 256-bit access), 16 of a 16-bit type, 8 of e4m3. Nothing is read twice, so
@@ -383,17 +379,6 @@ cudaError_t launch_adamw(const AdamWArgs& a, int dtype, int grad_dtype, int bits
                                   : launch_types<__nv_bfloat16, __nv_bfloat16>(a, bits, sms, s);
   return grad_dtype == FLCE_F32 ? launch_types<__half, float>(a, bits, sms, s)
                                 : launch_types<__half, __half>(a, bits, sms, s);
-}
-
-cudaError_t adamw_status(int** status) {
-  *status = nullptr;
-#ifdef FLCE_DEBUG
-  void* p = nullptr;
-  const cudaError_t e = cudaGetSymbolAddress(&p, g_adamw_status);
-  if (e != cudaSuccess) return e;
-  *status = static_cast<int*>(p);
-#endif
-  return cudaSuccess;
 }
 
 }  // namespace flce

@@ -14,7 +14,12 @@ using namespace flce;
 
 namespace {
 
-constexpr size_t kHeader = 256;   // status word at 0, finished-block counter at 8
+constexpr size_t kHeader = 256;          // of a workspace: the finished-block counter
+constexpr int kMaxBlocks = 1024;         // of the streaming and counting kernels
+
+#ifdef FLCE_DEBUG
+__device__ int g_debug_status;   // the bounds check's word: these entry points have no other errors
+#endif
 
 size_t elem_bytes(int dtype) { return dtype == FLCE_F32 ? 4 : 2; }
 
@@ -34,7 +39,8 @@ int check_tokens(const flce_tokens& t) {
     if (t.cu_seqlens == nullptr) return refuse(FLCE_ERR_INVALID_ARG, "cu_seqlens is NULL");
     if (!aligned(t.cu_seqlens, 4)) return refuse(FLCE_ERR_ALIGNMENT, "cu_seqlens");
   } else {
-    if (t.cols < 0 || (t.sequences > 0 && t.cols > (int64_t(1) << 40) / t.sequences))
+    if (t.cols < 0 || t.cols > 2147483647ll - 1024 ||
+        (t.sequences > 0 && t.cols > (int64_t(1) << 40) / t.sequences))
       return refuse(FLCE_ERR_INVALID_ARG, "cols");
     if (t.cu_seqlens != nullptr) return refuse(FLCE_ERR_INVALID_ARG, "cu_seqlens without packed");
   }
@@ -104,18 +110,40 @@ int check_policy(const flce_policy_args* a) {
   return FLCE_OK;
 }
 
+// A tensor of row stride ld whose offset of a token is its flat index.
+bool contiguous(const flce_tokens& t, const void* p, int64_t ld) {
+  return p == nullptr || t.packed || t.sequences <= 1 || ld == t.cols;
+}
+
+// Four neighbouring tokens, from a group's first one on, are aligned.
+bool groups_aligned(const flce_tokens& t, bool flat, const void* p, int64_t ld, size_t elem) {
+  return p == nullptr || (aligned(p, 4 * elem) && (flat || t.sequences <= 1 || ld % 4 == 0));
+}
+
 struct PolicyLayout {
-  size_t counts, loss, kl, clipped, total;
+  bool flat, small;
+  int64_t groups, row_groups, counts;   // counts: numbers in the count region
+  size_t counts_at, partials_at, total;
 };
 
 PolicyLayout policy_layout(const flce_policy_args* a) {
+  const flce_tokens& t = a->tokens;
   PolicyLayout L{};
-  const size_t S = static_cast<size_t>(a->tokens.sequences > 0 ? a->tokens.sequences : 2);
-  L.counts = kHeader;
-  L.loss = L.counts + S * 8;
-  L.kl = L.loss + S * 8;
-  L.clipped = L.kl + S * 8;
-  L.total = L.clipped + S * 8;
+  L.flat = contiguous(t, a->log_probs, a->ld_log_probs) && contiguous(t, a->old_log_probs, a->ld_old) &&
+           (a->kl_coef == 0.0 || contiguous(t, a->ref_log_probs, a->ld_ref)) &&
+           (!a->advantage_per_token || contiguous(t, a->advantages, a->ld_advantages)) &&
+           contiguous(t, a->grad, a->ld_grad) && contiguous(t, t.mask, t.ld_mask);
+  L.row_groups = t.packed ? 0 : (t.cols + 3) / 4;
+  L.groups = L.flat ? (token_total(t) + 3) / 4 : t.sequences * L.row_groups;
+  const bool masked = t.mask_kind != FLCE_MASK_NONE;
+  const bool by_sequence = a->reduction == FLCE_SEQUENCE_MEAN;
+  L.small = L.groups <= kPolicySmallGroups &&
+            !(masked && by_sequence && t.sequences > kPolicySmallSequences);
+  if (L.small) return L;
+  L.counts = !masked || a->reduction == FLCE_TOKEN_SUM ? 0 : by_sequence ? t.sequences : kMaxBlocks;
+  L.counts_at = kHeader;
+  L.partials_at = L.counts_at + (static_cast<size_t>(L.counts) * 8 + 15) / 16 * 16;
+  L.total = L.partials_at + kMaxBlocks * sizeof(PolicyPartial);
   return L;
 }
 
@@ -138,20 +166,22 @@ int check_preference(const flce_preference_args* a) {
 }
 
 struct PreferenceLayout {
-  size_t sums, counts, loss, total;
+  bool small;
+  size_t loss_at, total;
 };
 
 PreferenceLayout preference_layout(const flce_preference_args* a) {
   PreferenceLayout L{};
-  const size_t S = static_cast<size_t>(a->tokens.sequences > 0 ? a->tokens.sequences : 2);
-  L.sums = kHeader;
-  L.counts = L.sums + S * 8;
-  L.loss = L.counts + S * 8;
-  L.total = L.loss + S / 2 * 8;
+  const int64_t pairs = a->tokens.sequences / 2;
+  L.small = pairs <= kPreferenceSmallPairs && token_total(a->tokens) <= kPreferenceSmallTokens;
+  if (L.small) return L;
+  L.loss_at = kHeader;
+  L.total = L.loss_at + static_cast<size_t>(pairs) * 4;
   return L;
 }
 
 int check_workspace(const void* ws, uint64_t have, size_t need) {
+  if (need == 0) return FLCE_OK;
   if (ws == nullptr || have < need) return refuse(FLCE_ERR_WORKSPACE, "workspace");
   return aligned(ws, 16) ? FLCE_OK : refuse(FLCE_ERR_ALIGNMENT, "workspace");
 }
@@ -160,6 +190,21 @@ int cuda_error(cudaError_t e, const char* what) {
   char msg[200];
   snprintf(msg, sizeof(msg), "%s: %s", what, cudaGetErrorString(e));
   return refuse(FLCE_ERR_CUDA, msg);
+}
+
+// Debug builds: the zeroed word that the kernels flag bad stores in; else NULL.
+int debug_status(int** status, cudaStream_t s) {
+  *status = nullptr;
+#ifdef FLCE_DEBUG
+  void* p = nullptr;
+  cudaError_t e = cudaGetSymbolAddress(&p, g_debug_status);
+  if (e == cudaSuccess) e = cudaMemsetAsync(p, 0, sizeof(int), s);
+  if (e != cudaSuccess) return cuda_error(e, "the debug build's status word");
+  *status = static_cast<int*>(p);
+#else
+  (void)s;
+#endif
+  return FLCE_OK;
 }
 
 }  // namespace
@@ -220,32 +265,56 @@ int flce_policy_loss(const flce_policy_args* a, flce_stream_t stream) {
   k.sign = a->negated ? -1.f : 1.f;
   k.lo = static_cast<float>(log(1.0 - a->clip_low));
   k.hi = static_cast<float>(log(1.0 + a->clip_high));
+  k.ratio_lo = static_cast<float>(1.0 - a->clip_low);
+  k.ratio_hi = static_cast<float>(1.0 + a->clip_high);
   k.dual = static_cast<float>(a->dual_clip);
   k.log_dual = a->dual_clip > 0.0 ? static_cast<float>(log(a->dual_clip)) : 0.f;
   k.kl_coef = static_cast<float>(a->kl_coef);
   k.adv_per_token = a->advantage_per_token;
   k.kl = a->kl_estimator;
   k.reduction = a->reduction;
+  k.flat = L.flat ? 1 : 0;
+  k.vec = groups_aligned(t, L.flat, a->log_probs, a->ld_log_probs, elem) &&
+          groups_aligned(t, L.flat, a->old_log_probs, a->ld_old, elem) &&
+          (a->kl_coef == 0.0 || groups_aligned(t, L.flat, a->ref_log_probs, a->ld_ref, elem)) &&
+          (!a->advantage_per_token || groups_aligned(t, L.flat, a->advantages, a->ld_advantages, 4));
+  k.vec_mask = t.mask_kind == FLCE_MASK_BYTES && groups_aligned(t, L.flat, t.mask, t.ld_mask, 1);
+  k.vec_grad = groups_aligned(t, L.flat, a->grad, a->ld_grad, 4);
+  k.groups = L.groups;
+  k.row_groups = L.row_groups;
   k.loss = a->loss;
   k.num_tokens = a->num_tokens;
   k.num_clipped = a->num_clipped;
   k.kl_sum = a->kl_sum;
-  k.status = reinterpret_cast<int*>(ws);
-  k.done = reinterpret_cast<int*>(ws + 8);
-  k.counts = reinterpret_cast<long long*>(ws + L.counts);
-  k.part_loss = reinterpret_cast<double*>(ws + L.loss);
-  k.part_kl = reinterpret_cast<double*>(ws + L.kl);
-  k.part_clipped = reinterpret_cast<long long*>(ws + L.clipped);
   k.r_grad = DevRegion{a->grad, span(t, a->ld_grad) * 4};
   k.r_ws = DevRegion{ws, L.total};
+  if ((v = debug_status(&k.status, st)) != FLCE_OK) return v;
 
-  cudaError_t e = cudaMemsetAsync(ws, 0, kHeader, st);
-  if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync");
-  if ((v = run_kernel("flce_token_count", st, [&] { return launch_token_count(k, st); })) != FLCE_OK)
-    return v;
-  if ((v = run_kernel("flce_policy", st, [&] { return launch_policy(k, a->dtype, st); })) != FLCE_OK)
-    return v;
-  return finish_call(ws, st);
+  if (L.small) {
+    v = run_kernel("flce_policy_small", st, [&] { return launch_policy_small(k, a->dtype, st); });
+    return v != FLCE_OK ? v : finish_call(k.status, st);
+  }
+  const int64_t most = std::min<int64_t>(kMaxBlocks, int64_t(sms) * kPolicyBlocksPerSm);
+  k.per = (L.groups + most - 1) / most;
+  k.per = (k.per + 255) / 256 * 256;   // whole rounds of a block's threads
+  const unsigned grid = static_cast<unsigned>((L.groups + k.per - 1) / k.per);
+  k.done = reinterpret_cast<int*>(ws);
+  k.counts = reinterpret_cast<long long*>(ws + L.counts_at);
+  k.num_counts = L.counts;
+  k.partials = reinterpret_cast<PolicyPartial*>(ws + L.partials_at);
+  if (L.counts > 0) {
+    const int64_t work = a->reduction == FLCE_SEQUENCE_MEAN ? t.sequences : (L.groups + 1023) / 1024;
+    const int blocks = static_cast<int>(std::min<int64_t>(work, most));
+    if (a->reduction == FLCE_TOKEN_MEAN) k.num_counts = blocks;
+    v = run_kernel("flce_policy_count", st, [&] { return launch_count(k, blocks, st); });
+    if (v != FLCE_OK) return v;
+  } else {
+    const cudaError_t e = cudaMemsetAsync(k.done, 0, sizeof(int), st);
+    if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync");
+  }
+  v = run_kernel("flce_policy", st,
+                 [&] { return launch_policy(k, a->dtype, L.counts > 0, grid, st); });
+  return v != FLCE_OK ? v : finish_call(k.status, st);
 }
 
 int flce_preference_workspace_bytes(const flce_preference_args* a, size_t* bytes) {
@@ -285,31 +354,46 @@ int flce_preference_loss(const flce_preference_args* a, flce_stream_t stream) {
   k.ld_ref = a->ld_ref;
   k.ld_grad = a->ld_grad;
   k.sign = a->negated ? -1.f : 1.f;
-  k.beta = a->beta;
-  k.smoothing = a->label_smoothing;
-  k.margin = a->margin;
+  k.beta = static_cast<float>(a->beta);
+  k.smoothing = static_cast<float>(a->label_smoothing);
+  k.margin = static_cast<float>(a->margin);
   k.type = a->loss_type;
   k.average = a->average;
   k.loss = a->loss;
   k.chosen = a->chosen_rewards;
   k.rejected = a->rejected_rewards;
-  k.status = reinterpret_cast<int*>(ws);
-  k.done = reinterpret_cast<int*>(ws + 8);
-  k.sums = reinterpret_cast<double*>(ws + L.sums);
-  k.counts = reinterpret_cast<long long*>(ws + L.counts);
-  k.pair_loss = reinterpret_cast<double*>(ws + L.loss);
+  k.flat = contiguous(t, a->log_probs, a->ld_log_probs) && contiguous(t, a->ref_log_probs, a->ld_ref) &&
+           contiguous(t, a->grad, a->ld_grad) && contiguous(t, t.mask, t.ld_mask);
+  k.vec = groups_aligned(t, k.flat, a->log_probs, a->ld_log_probs, elem) &&
+          groups_aligned(t, k.flat, a->ref_log_probs, a->ld_ref, elem);
+  k.vec_mask = t.mask_kind == FLCE_MASK_BYTES && groups_aligned(t, k.flat, t.mask, t.ld_mask, 1);
+  k.vec_grad = groups_aligned(t, k.flat, a->grad, a->ld_grad, 4);
   k.r_grad = DevRegion{a->grad, span(t, a->ld_grad) * 4};
   k.r_ws = DevRegion{ws, L.total};
+  if ((v = debug_status(&k.status, st)) != FLCE_OK) return v;
 
-  cudaError_t e = cudaMemsetAsync(ws, 0, kHeader, st);
+  const int64_t pairs = t.sequences / 2;
+  if (pairs == 0 && t.packed && t.tokens > 0 && a->grad != nullptr) {
+    // no pair writes the tokens outside every sequence
+    const cudaError_t e = cudaMemsetAsync(a->grad, 0, static_cast<size_t>(t.tokens) * 4, st);
+    if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync");
+  }
+  if (L.small || pairs == 0) {
+    v = run_kernel("flce_preference_small", st,
+                   [&] { return launch_preference_small(k, a->dtype, st); });
+    return v != FLCE_OK ? v : finish_call(k.status, st);
+  }
+  k.done = reinterpret_cast<int*>(ws);
+  k.pair_loss = reinterpret_cast<float*>(ws + L.loss_at);
+  // Blocks a pair: enough to fill the GPU several times over, while each still
+  // has a few rounds of its threads to do.
+  const int64_t a_pair = token_total(t) / pairs;
+  int cluster = 1;
+  while (cluster < 8 && pairs * cluster < 6 * sms && a_pair / (cluster * 2) >= 4096) cluster *= 2;
+  const cudaError_t e = cudaMemsetAsync(k.done, 0, sizeof(int), st);
   if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync");
-  if ((v = run_kernel("flce_sequence_sum", st,
-                      [&] { return launch_sequence_sum(k, a->dtype, st); })) != FLCE_OK)
-    return v;
-  if ((v = run_kernel("flce_preference", st,
-                      [&] { return launch_preference(k, a->dtype, st); })) != FLCE_OK)
-    return v;
-  return finish_call(ws, st);
+  v = run_kernel("flce_preference", st, [&] { return launch_preference(k, a->dtype, cluster, st); });
+  return v != FLCE_OK ? v : finish_call(k.status, st);
 }
 
 int flce_adamw(const flce_adamw_args* a, flce_stream_t stream) {
@@ -359,10 +443,7 @@ int flce_adamw(const flce_adamw_args* a, flce_stream_t stream) {
   cudaStream_t st = reinterpret_cast<cudaStream_t>(stream);
 
   AdamWArgs k;
-  cudaError_t e = adamw_status(&k.status);
-  if (e != cudaSuccess) return cuda_error(e, "cudaGetSymbolAddress");
-  if (k.status != nullptr && (e = cudaMemsetAsync(k.status, 0, sizeof(int), st)) != cudaSuccess)
-    return cuda_error(e, "cudaMemsetAsync");
+  if ((v = debug_status(&k.status, st)) != FLCE_OK) return v;
   k.grad_scale = a->grad_scale;
   k.decay = static_cast<float>(1.0 - a->lr * a->weight_decay);
   k.step_size = static_cast<float>(a->lr / (1.0 - pow(a->beta1, static_cast<double>(a->step))));

@@ -34,30 +34,50 @@ struct TokenView {
   int mask_kind;
 };
 
+// A block's share of the reduced outputs.
+struct __align__(16) PolicyPartial {
+  float loss, loss_err, kl, kl_err;   // sums and their rounding errors
+  long long both;                     // clipped tokens, and in the low 32 bits tokens that count
+};
+
+constexpr int kPolicySmallGroups = 8192;      // groups of 4 tokens in one cluster of 8 x 1024 threads
+constexpr int kPolicySmallSequences = 1024;   // sequences whose tokens it can count ("sequence_mean")
+constexpr int kPolicyBlocksPerSm = 4;
+
 struct PolicyArgs {
   TokenView t;
   const void* lp;
   const void* old;             // nullable
-  const void* ref;             // nullable
+  const void* ref;             // nullable; read when kl_coef is not 0
   const float* adv;
   float* grad;                 // nullable
   long long ld_lp, ld_old, ld_ref, ld_adv, ld_grad;
   float sign;                  // -1: lp holds -log p
-  float lo, hi, log_dual, dual, kl_coef;   // dual: 0 off
+  float lo, hi, ratio_lo, ratio_hi, log_dual, dual, kl_coef;   // dual: 0 off
   int adv_per_token, kl, reduction;
+  // Every token tensor is contiguous: a token has the same offset in all.
+  // Else a token's offset is row * ld + column.
+  int flat;
+  // Four neighbours are aligned in the inputs; in the mask; in grad.
+  int vec, vec_mask, vec_grad;
+  long long groups;            // of 4 tokens: flat (N + 3) / 4, else S * row_groups
+  long long row_groups;        // (cols + 3) / 4
   float* loss;
   int64_t* num_tokens;
   int64_t* num_clipped;
   float* kl_sum;
-  // workspace
-  int* status;
-  int* done;                   // zeroed before the main kernel
-  long long* counts;           // [S]
-  double* part_loss;           // [S]
-  double* part_kl;
-  long long* part_clipped;
+  int* status;                 // nullable; written by FLCE_DEBUG builds
+  // Large batches
+  long long per;               // groups a block of the streaming kernel
+  int* done;                   // 0 before the streaming kernel
+  long long* counts;           // tokens that count: num_counts parts, or one a sequence
+  long long num_counts;        // 0: no mask
+  PolicyPartial* partials;     // one a block
   DevRegion r_grad, r_ws;
 };
+
+constexpr long long kPreferenceSmallTokens = 65536;
+constexpr long long kPreferenceSmallPairs = 64;
 
 struct PreferenceArgs {
   TokenView t;
@@ -66,23 +86,25 @@ struct PreferenceArgs {
   float* grad;                 // nullable
   long long ld_lp, ld_ref, ld_grad;
   float sign;
+  int flat, vec, vec_mask, vec_grad;   // as PolicyArgs
   float beta, smoothing, margin;
   int type, average;
   float* loss;
   float* chosen;               // nullable
   float* rejected;             // nullable
   int* status;
-  int* done;
-  double* sums;                // [S]
-  long long* counts;           // [S]
-  double* pair_loss;           // [S / 2]
+  int* done;                   // large batches: 0 before the kernel
+  float* pair_loss;            // [S / 2]
   DevRegion r_grad, r_ws;
 };
 
-cudaError_t launch_token_count(const PolicyArgs& a, cudaStream_t s);
-cudaError_t launch_policy(const PolicyArgs& a, int dtype, cudaStream_t s);
-cudaError_t launch_sequence_sum(const PreferenceArgs& a, int dtype, cudaStream_t s);
-cudaError_t launch_preference(const PreferenceArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_policy_small(const PolicyArgs& a, int dtype, cudaStream_t s);
+cudaError_t launch_count(const PolicyArgs& a, int blocks, cudaStream_t s);
+// after_count: launch_count is the kernel right before it in the stream.
+cudaError_t launch_policy(const PolicyArgs& a, int dtype, bool after_count, unsigned grid, cudaStream_t s);
+cudaError_t launch_preference_small(const PreferenceArgs& a, int dtype, cudaStream_t s);
+// cluster: blocks a pair (1, 2, 4 or 8).
+cudaError_t launch_preference(const PreferenceArgs& a, int dtype, int cluster, cudaStream_t s);
 
 struct AdamWArgs {
   const float* grad_scale;     // nullable
@@ -101,6 +123,5 @@ struct AdamWArgs {
 // dtype and grad_dtype: flce_dtype; bits: 8 or 32.
 cudaError_t launch_adamw(const AdamWArgs& a, int dtype, int grad_dtype, int bits, int sms,
                          cudaStream_t s);
-cudaError_t adamw_status(int** status);   // debug builds: a device word for the bounds check
 
 }  // namespace flce

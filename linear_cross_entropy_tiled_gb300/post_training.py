@@ -15,7 +15,6 @@ include/flce.h gives the formulas.
 """
 from __future__ import annotations
 
-import ctypes
 from typing import Optional
 
 import torch
@@ -24,11 +23,11 @@ from . import _lib
 from .functional import (_DTYPES, _maybe_check, _params, _prepare, _ptr, _stream, flce_backward,
                          flce_forward)
 
+_SMALL = 8192   # tokens; batches of no more need no workspace (include/flce.h)
 
-def _laid_out(t: Optional[torch.Tensor], shape, dtype, device, name: str):
+
+def _laid_out(t: torch.Tensor, shape, dtype, device, name: str):
     """(tensor, row stride) of a token tensor; anything but adjacent tokens in a row is copied."""
-    if t is None:
-        return None, 0
     if t.shape != shape:
         raise ValueError(f"{name} must have the shape of the log probabilities, {tuple(shape)}, "
                          f"got {tuple(t.shape)}")
@@ -36,41 +35,51 @@ def _laid_out(t: Optional[torch.Tensor], shape, dtype, device, name: str):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}")
-    if t.dim() == 1:
-        return t.contiguous(), 0
-    if t.shape[1] > 1 and t.stride(1) != 1 or t.stride(0) < t.shape[1]:
-        t = t.contiguous()
-    return t, max(t.stride(0), t.shape[1])
+    cols = shape[-1]
+    if t.is_contiguous():
+        return t, cols
+    if len(shape) == 1 or (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
+        return t.contiguous(), cols
+    return t, t.stride(0)
 
 
-def _token_fields(x: torch.Tensor, mask, cu_seqlens, name: str):
-    """flce_tokens of the batch, the number of sequences, and the tensors it points to."""
+def _tokens(x: torch.Tensor, mask, cu_seqlens, name: str):
+    """The fields of flce_tokens, the number of sequences, and the tensors they point to."""
     if not x.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
     if x.dtype not in _DTYPES:
         raise TypeError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
-    t = _lib.FlceTokens()
-    cu = None
+    shape = x.shape
     if cu_seqlens is None:
-        if x.dim() != 2:
+        if len(shape) != 2:
             raise ValueError(f"{name} must be [sequences, cols], or [tokens] with cu_seqlens; "
-                             f"got {tuple(x.shape)}")
-        t.sequences, t.cols = x.shape
+                             f"got {tuple(shape)}")
+        sequences, cols = shape
+        tokens = packed = cu = 0
     else:
-        if x.dim() != 1:
-            raise ValueError(f"{name} must be [tokens] with cu_seqlens, got {tuple(x.shape)}")
+        if len(shape) != 1:
+            raise ValueError(f"{name} must be [tokens] with cu_seqlens, got {tuple(shape)}")
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.device != x.device:
             raise ValueError(f"cu_seqlens must be [sequences + 1] on {x.device}")
         if cu_seqlens.dtype not in (torch.int32, torch.int64):
             raise TypeError(f"cu_seqlens must be int32 or int64, got {cu_seqlens.dtype}")
-        cu = cu_seqlens.to(torch.int32).contiguous()
-        t.packed, t.sequences, t.tokens, t.cu_seqlens = 1, cu.shape[0] - 1, x.shape[0], cu.data_ptr()
+        cu_seqlens = cu_seqlens.to(torch.int32).contiguous()
+        sequences, cols, tokens, packed = cu_seqlens.shape[0] - 1, 0, shape[0], 1
+        cu = cu_seqlens.data_ptr()
+    where = kind = ld = 0
     if mask is not None:
-        if mask.dtype not in (torch.bool, torch.uint8):
+        if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
             raise TypeError(f"mask must be bool or uint8, got {mask.dtype}")
-        mask, t.ld_mask = _laid_out(mask, x.shape, mask.dtype, x.device, "mask")
-        t.mask, t.mask_kind = _ptr(mask), _lib.FLCE_MASK_BYTES
-    return t, int(t.sequences), (cu, mask)
+        mask, ld = _laid_out(mask, shape, mask.dtype, x.device, "mask")
+        where, kind = mask.data_ptr(), _lib.FLCE_MASK_BYTES
+    return (sequences, cols, tokens, cu, where, ld, 0, packed, kind), sequences, (cu_seqlens, mask)
+
+
+def _label_tokens(nll, labels, ignore_index, cu_seqlens):
+    """``_tokens`` for log probabilities of ``labels`` (contiguous): those that are ignored do not count."""
+    (sequences, cols, tokens, cu, *_, packed, _), n, keep = _tokens(nll, None, cu_seqlens, "targets")
+    return (sequences, cols, tokens, cu, labels.data_ptr(), labels.shape[-1], ignore_index, packed,
+            _lib.FLCE_MASK_LABELS), n, keep
 
 
 def _option(table: dict, value: str, name: str) -> int:
@@ -79,49 +88,56 @@ def _option(table: dict, value: str, name: str) -> int:
     return table[value]
 
 
-def _run_policy(a: _lib.FlcePolicyArgs, dev: torch.device, return_metrics: bool):
-    out = torch.empty(2, dtype=torch.float32, device=dev)
-    a.loss = out.data_ptr()
-    metrics = None
-    if return_metrics:
-        n = torch.empty(2, dtype=torch.int64, device=dev)
-        a.num_tokens, a.num_clipped, a.kl_sum = n.data_ptr(), n.data_ptr() + 8, out.data_ptr() + 4
-        metrics = {"num_tokens": n[0], "num_clipped": n[1], "kl_sum": out[1]}
-    ws = torch.empty(_lib.policy_workspace_bytes(a), dtype=torch.uint8, device=dev)
-    a.workspace, a.ws_bytes = ws.data_ptr(), ws.numel()
-    _lib.check(_lib.policy_loss_raw(a, _stream(dev)), "flce_policy_loss")
-    return out[0], metrics
-
-
-def _policy_args(tokens, log_probs, ld, old, advantages, ref, clip_low, clip_high, dual_clip,
-                 kl_coef, kl_estimator, reduction, grad):
-    """FlcePolicyArgs without its outputs but ``grad``, and the tensors it points to."""
+def _policy(tokens, sequences, log_probs, old, advantages, ref, clip_low, clip_high, dual_clip,
+            kl_coef, kl_estimator, reduction, return_metrics, negated):
+    """(loss, grad, metrics or None) of flce_policy_loss on ``tokens``."""
     shape, dtype, dev = log_probs.shape, log_probs.dtype, log_probs.device
-    a = _lib.FlcePolicyArgs()
-    a.tokens = tokens
-    a.kl_estimator = _option(_lib.KL_ESTIMATORS, kl_estimator, "kl_estimator")
-    a.reduction = _option(_lib.TOKEN_REDUCTIONS, reduction, "reduction")
-    if kl_coef and ref is None:
-        raise ValueError("kl_coef needs ref_log_probs")
+    estimator = _option(_lib.KL_ESTIMATORS, kl_estimator, "kl_estimator")
+    reduce = _option(_lib.TOKEN_REDUCTIONS, reduction, "reduction")
+    log_probs, ld = _laid_out(log_probs, shape, dtype, dev, "log_probs")
     if advantages.dtype != torch.float32 or advantages.device != dev:
         raise TypeError(f"advantages must be float32 on {dev}")
-    S = tokens.sequences
-    if advantages.shape == (S,) and not (tokens.packed and shape == (S,)) \
-            or advantages.shape == (S, 1) and shape[-1] != 1:
-        advantages, ld_adv = advantages.reshape(S).contiguous(), 0
+    a_shape, ld_adv, per_token = advantages.shape, 0, 0
+    if a_shape == shape:
+        advantages, ld_adv = _laid_out(advantages, shape, torch.float32, dev, "advantages")
+        per_token = 1
+    elif a_shape == (sequences,) or a_shape == (sequences, 1):
+        advantages = advantages.reshape(sequences).contiguous()
     else:
-        advantages, ld_adv = _laid_out(advantages, shape, torch.float32, dev,
-                                       "advantages, unless it is one per sequence,")
-        a.advantage_per_token = 1
-    old, a.ld_old = _laid_out(old, shape, dtype, dev, "old_log_probs")
-    ref, a.ld_ref = _laid_out(ref, shape, dtype, dev, "ref_log_probs")
-    a.log_probs, a.ld_log_probs = _ptr(log_probs), ld
-    a.old_log_probs, a.ref_log_probs, a.advantages = _ptr(old), _ptr(ref), _ptr(advantages)
-    a.ld_advantages = ld_adv
-    a.grad, a.ld_grad = _ptr(grad), shape[-1]
-    a.clip_low, a.clip_high, a.dual_clip = clip_low, clip_high, dual_clip or 0.0
-    a.kl_coef, a.dtype = kl_coef, _DTYPES[dtype]
-    return a, (old, ref, advantages)
+        raise ValueError(f"advantages must be [{sequences}], one per sequence, or {tuple(shape)}, "
+                         f"one per token; got {tuple(a_shape)}")
+    old_at = ref_at = ld_old = ld_ref = 0
+    if old is not None:
+        old, ld_old = _laid_out(old, shape, dtype, dev, "old_log_probs")
+        old_at = old.data_ptr()
+    if ref is not None:
+        ref, ld_ref = _laid_out(ref, shape, dtype, dev, "ref_log_probs")
+        ref_at = ref.data_ptr()
+    elif kl_coef:
+        raise ValueError("kl_coef needs ref_log_probs")
+    grad = torch.empty(shape, dtype=torch.float32, device=dev)
+    out = torch.empty(2, dtype=torch.float32, device=dev)
+    loss_at = out.data_ptr()
+    kl_at = n_at = clipped_at = 0
+    if return_metrics:
+        n = torch.empty(2, dtype=torch.int64, device=dev)
+        kl_at, n_at = loss_at + 4, n.data_ptr()
+        clipped_at = n_at + 8
+
+    def pack(ws, ws_bytes):
+        return _lib.POLICY_ARGS.pack(
+            *tokens, log_probs.data_ptr(), old_at, ref_at, advantages.data_ptr(), loss_at,
+            grad.data_ptr(), n_at, clipped_at, kl_at, ws, ws_bytes, ld, ld_old, ld_ref, ld_adv,
+            shape[-1], clip_low, clip_high, dual_clip or 0.0, kl_coef, _DTYPES[dtype], per_token,
+            estimator, reduce, negated, 0)
+    args = pack(0, 0)
+    if grad.numel() > _SMALL or sequences > 1024:
+        ws = torch.empty(max(16, _lib.policy_workspace_bytes(args)), dtype=torch.uint8, device=dev)
+        args = pack(ws.data_ptr(), ws.numel())
+    _lib.check(_lib.policy_loss_raw(args, _stream(dev)), "flce_policy_loss")
+    if not return_metrics:
+        return out[0], grad, None
+    return out[0], grad, {"num_tokens": n[0], "num_clipped": n[1], "kl_sum": out[1]}
 
 
 def policy_loss_and_grad(log_probs: torch.Tensor, old_log_probs: Optional[torch.Tensor],
@@ -136,50 +152,52 @@ def policy_loss_and_grad(log_probs: torch.Tensor, old_log_probs: Optional[torch.
 
     ``old_log_probs`` (None: the policy drew the tokens itself) and
     ``ref_log_probs`` have the shape and dtype of ``log_probs``;
-    ``advantages`` is float32, one per sequence or one per token. (A packed
-    batch of as many sequences as tokens reads it as one per token; the two
-    are the same there unless a sequence is empty.)
+    ``advantages`` is float32, of the shape of ``log_probs`` or one per
+    sequence, ``[sequences]``. (Of a packed batch of as many sequences as
+    tokens it is read as one per token; unless a sequence is empty, that is
+    the same.)
     ``reduction``: "sum", "mean" over the tokens that count, or
     "sequence_mean", the mean over sequences of each one's mean.
 
     Returns ``(loss, grad)``, both float32, or ``(loss, grad, metrics)`` with
     the device scalars num_tokens, num_clipped (int64) and kl_sum.
     """
-    tokens, _, keep = _token_fields(log_probs, mask, cu_seqlens, "log_probs")
-    log_probs, ld = _laid_out(log_probs, log_probs.shape, log_probs.dtype, log_probs.device,
-                              "log_probs")
-    grad = torch.empty(log_probs.shape, dtype=torch.float32, device=log_probs.device)
-    a, keep2 = _policy_args(tokens, log_probs, ld, old_log_probs, advantages, ref_log_probs,
-                            clip_low, clip_high, dual_clip, kl_coef, kl_estimator, reduction, grad)
-    loss, metrics = _run_policy(a, log_probs.device, return_metrics)
+    tokens, sequences, keep = _tokens(log_probs, mask, cu_seqlens, "log_probs")
+    loss, grad, metrics = _policy(tokens, sequences, log_probs, old_log_probs, advantages,
+                                  ref_log_probs, clip_low, clip_high, dual_clip, kl_coef,
+                                  kl_estimator, reduction, return_metrics, 0)
     return (loss, grad, metrics) if return_metrics else (loss, grad)
 
 
-def _run_preference(a: _lib.FlcePreferenceArgs, dev: torch.device, pairs: int):
-    out = torch.empty(1 + 2 * pairs, dtype=torch.float32, device=dev)
-    a.loss, a.chosen_rewards = out.data_ptr(), out.data_ptr() + 4
-    a.rejected_rewards = out.data_ptr() + 4 + 4 * pairs
-    ws = torch.empty(_lib.preference_workspace_bytes(a), dtype=torch.uint8, device=dev)
-    a.workspace, a.ws_bytes = ws.data_ptr(), ws.numel()
-    _lib.check(_lib.preference_loss_raw(a, _stream(dev)), "flce_preference_loss")
-    return out[0], out[1:1 + pairs], out[1 + pairs:]
-
-
-def _preference_args(tokens, log_probs, ld, ref, beta, loss_type, label_smoothing, margin, average,
-                     grad):
-    if tokens.sequences % 2:
+def _preference(tokens, sequences, log_probs, ref, beta, loss_type, label_smoothing, margin,
+                average, negated):
+    """(loss, grad, chosen rewards, rejected rewards) of flce_preference_loss on ``tokens``."""
+    if sequences % 2:
         raise ValueError("a preference batch needs an even number of sequences: the chosen ones, "
                          "then the rejected ones")
-    shape = log_probs.shape
-    a = _lib.FlcePreferenceArgs()
-    a.tokens = tokens
-    a.loss_type = _option(_lib.PREFERENCE_LOSSES, loss_type, "loss_type")
-    ref, a.ld_ref = _laid_out(ref, shape, log_probs.dtype, log_probs.device, "ref_log_probs")
-    a.log_probs, a.ld_log_probs, a.ref_log_probs = _ptr(log_probs), ld, _ptr(ref)
-    a.grad, a.ld_grad = _ptr(grad), shape[-1]
-    a.beta, a.label_smoothing, a.margin = beta, label_smoothing, margin
-    a.dtype, a.average = _DTYPES[log_probs.dtype], 1 if average else 0
-    return a, ref
+    shape, dtype, dev = log_probs.shape, log_probs.dtype, log_probs.device
+    kind = _option(_lib.PREFERENCE_LOSSES, loss_type, "loss_type")
+    log_probs, ld = _laid_out(log_probs, shape, dtype, dev, "log_probs")
+    ref_at = ld_ref = 0
+    if ref is not None:
+        ref, ld_ref = _laid_out(ref, shape, dtype, dev, "ref_log_probs")
+        ref_at = ref.data_ptr()
+    pairs = sequences // 2
+    grad = torch.empty(shape, dtype=torch.float32, device=dev)
+    out = torch.empty(1 + 2 * pairs, dtype=torch.float32, device=dev)
+    at = out.data_ptr()
+
+    def pack(ws, ws_bytes):
+        return _lib.PREFERENCE_ARGS.pack(
+            *tokens, log_probs.data_ptr(), ref_at, at, grad.data_ptr(), at + 4, at + 4 + 4 * pairs,
+            ws, ws_bytes, ld, ld_ref, shape[-1], beta, label_smoothing, margin, _DTYPES[dtype], kind,
+            1 if average else 0, negated)
+    args = pack(0, 0)
+    if grad.numel() > _SMALL or pairs > 64:
+        ws = torch.empty(max(16, _lib.preference_workspace_bytes(args)), dtype=torch.uint8, device=dev)
+        args = pack(ws.data_ptr(), ws.numel())
+    _lib.check(_lib.preference_loss_raw(args, _stream(dev)), "flce_preference_loss")
+    return out[0], grad, out[1:1 + pairs], out[1 + pairs:]
 
 
 def preference_loss_and_grad(log_probs: torch.Tensor, ref_log_probs: Optional[torch.Tensor] = None,
@@ -196,14 +214,9 @@ def preference_loss_and_grad(log_probs: torch.Tensor, ref_log_probs: Optional[to
     Returns ``(loss, grad, chosen_rewards, rejected_rewards)``, all float32;
     the rewards are beta times each sequence's log ratio.
     """
-    tokens, sequences, keep = _token_fields(log_probs, mask, cu_seqlens, "log_probs")
-    log_probs, ld = _laid_out(log_probs, log_probs.shape, log_probs.dtype, log_probs.device,
-                              "log_probs")
-    grad = torch.empty(log_probs.shape, dtype=torch.float32, device=log_probs.device)
-    a, keep2 = _preference_args(tokens, log_probs, ld, ref_log_probs, beta, loss_type,
-                                label_smoothing, margin, average, grad)
-    loss, chosen, rejected = _run_preference(a, log_probs.device, sequences // 2)
-    return loss, grad, chosen, rejected
+    tokens, sequences, keep = _tokens(log_probs, mask, cu_seqlens, "log_probs")
+    return _preference(tokens, sequences, log_probs, ref_log_probs, beta, loss_type,
+                       label_smoothing, margin, average, 0)
 
 
 def _scaled(grad: torch.Tensor, grad_loss: torch.Tensor) -> torch.Tensor:
@@ -279,13 +292,6 @@ class _FusedLinear(torch.autograd.Function):
         return None if gh is None else gh.reshape(ctx.hidden_shape), gw, gb, None, None, None
 
 
-def _label_tokens(nll, labels, ignore_index, cu_seqlens):
-    tokens, sequences, keep = _token_fields(nll, None, cu_seqlens, "targets")
-    tokens.mask, tokens.mask_kind = labels.data_ptr(), _lib.FLCE_MASK_LABELS
-    tokens.ld_mask, tokens.ignore_index = labels.shape[-1], ignore_index
-    return tokens, sequences, keep
-
-
 def fused_linear_policy_loss(hidden: torch.Tensor, weight: torch.Tensor, targets: torch.Tensor,
                              old_log_probs: Optional[torch.Tensor], advantages: torch.Tensor, *,
                              bias: Optional[torch.Tensor] = None,
@@ -306,13 +312,10 @@ def fused_linear_policy_loss(hidden: torch.Tensor, weight: torch.Tensor, targets
     gradients; the logits are never stored.
     """
     def fn(nll, labels):
-        tokens, _, keep = _label_tokens(nll, labels, ignore_index, cu_seqlens)
-        grad = torch.empty_like(nll)
-        a, keep2 = _policy_args(tokens, nll, nll.shape[-1], old_log_probs, advantages, ref_log_probs,
+        tokens, sequences, keep = _label_tokens(nll, labels, ignore_index, cu_seqlens)
+        loss, grad, m = _policy(tokens, sequences, nll, old_log_probs, advantages, ref_log_probs,
                                 clip_low, clip_high, dual_clip, kl_coef, kl_estimator, reduction,
-                                grad)
-        a.negated = 1
-        loss, m = _run_policy(a, nll.device, True)
+                                True, 1)
         return (loss, grad, *(m[k] for k in _METRICS))
     loss, *m = _FusedLinear.apply(hidden, weight, bias, targets, (ignore_index, logit_scale, softcap),
                                   fn)
@@ -335,10 +338,6 @@ def fused_linear_preference_loss(hidden: torch.Tensor, weight: torch.Tensor, tar
     """
     def fn(nll, labels):
         tokens, sequences, keep = _label_tokens(nll, labels, ignore_index, cu_seqlens)
-        grad = torch.empty_like(nll)
-        a, keep2 = _preference_args(tokens, nll, nll.shape[-1], ref_log_probs, beta, loss_type,
-                                    label_smoothing, margin, average, grad)
-        a.negated = 1
-        loss, chosen, rejected = _run_preference(a, nll.device, sequences // 2)
-        return loss, grad, chosen, rejected
+        return _preference(tokens, sequences, nll, ref_log_probs, beta, loss_type, label_smoothing,
+                           margin, average, 1)
     return _FusedLinear.apply(hidden, weight, bias, targets, (ignore_index, logit_scale, softcap), fn)

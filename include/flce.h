@@ -490,9 +490,10 @@ typedef enum {
 
 typedef struct {
   int64_t sequences;         /* >= 0 and <= 2^30                                  */
-  int64_t cols;              /* padded: tokens a row, >= 0; packed: ignored       */
+  int64_t cols;              /* padded: tokens a row, 0 to 2^31 - 1025; packed:
+                                ignored                                           */
   int64_t tokens;            /* packed: tokens in all, <= 2^31 - 1024; padded:
-                                ignored (sequences * cols <= 2^40)                */
+                                ignored (sequences * cols <= 2^39)                */
   const int32_t* cu_seqlens; /* packed: device int32 [sequences + 1], else NULL   */
   const void* mask;          /* as mask_kind says; NULL with FLCE_MASK_NONE       */
   int64_t ld_mask;           /* row stride of the mask, in its elements (padded)  */

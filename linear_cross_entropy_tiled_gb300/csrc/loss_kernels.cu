@@ -21,6 +21,7 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include "elements.cuh"
 #include "post_training.h"
 #include "ptx.cuh"
 
@@ -31,7 +32,10 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;          // streaming and counting kernels
 constexpr int kSmallThreads = 1024;    // policy_small_kernel
-constexpr int kPairThreads = 512;      // preference kernels
+#ifndef PTH
+#define PTH 256
+#endif
+constexpr int kPairThreads = PTH;      // preference kernels
 constexpr int kCluster = 8;
 
 // ------------------------------------------------------------- reductions
@@ -75,16 +79,15 @@ __device__ __forceinline__ V block_total(V v) {
   return r;
 }
 
-// True in every thread of the last block of the grid to get here (each block
-// makes its stores visible before it counts itself).
-__device__ __forceinline__ bool last_block(int* done) {
-  __shared__ int s_last;
+// Thread 0 has stored its block's share of the outputs and counts it on
+// `done`; true there if all `expected` shares have now been counted, and so
+// visible to this thread. (The fence waits for that thread's stores alone,
+// not for the block's gradients.)
+__device__ __forceinline__ bool counted_last(int* done, int expected) {
   __threadfence();
-  __syncthreads();
-  if (threadIdx.x == 0) s_last = atomicAdd(done, 1) == static_cast<int>(gridDim.x) - 1;
-  __syncthreads();
-  if (s_last) __threadfence();
-  return s_last != 0;
+  const bool last = atomicAdd(done, 1) == expected - 1;
+  __threadfence();
+  return last;
 }
 
 // Programmatic dependent launch: the next kernel of the stream may start; this
@@ -97,10 +100,6 @@ __device__ __forceinline__ void wait_for_previous() {
 }
 
 // ------------------------------------------------------- groups of 4 tokens
-__device__ __forceinline__ float to_f32(float x) { return x; }
-__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
-
 __device__ __forceinline__ void load4_vec(const float* p, float (&x)[4]) {
   const float4 v = __ldg(reinterpret_cast<const float4*>(p));
   x[0] = v.x;
@@ -116,7 +115,7 @@ __device__ __forceinline__ void load4_vec(const T* p, float (&x)[4]) {
   x[2] = Elem<T>::lo(v.y);
   x[3] = Elem<T>::hi(v.y);
 }
-// The tokens of `bits`; the others read as 0. `vec`: p is aligned to four
+// The tokens of `bits`; the others are left alone. `vec`: p is aligned to four
 // elements and all four are in the tensor.
 template <typename T>
 __device__ __forceinline__ void load4(const T* p, unsigned bits, bool vec, float (&x)[4]) {
@@ -125,7 +124,8 @@ __device__ __forceinline__ void load4(const T* p, unsigned bits, bool vec, float
     return;
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) x[k] = bits >> k & 1u ? to_f32(p[k]) : 0.f;
+  for (int k = 0; k < 4; ++k)
+    if (bits >> k & 1u) x[k] = to_f32(p[k]);
 }
 // The tokens of `range` (a subset of the four). `r`: the tensor the store must
 // stay in (checked in FLCE_DEBUG builds).
@@ -141,16 +141,19 @@ __device__ __forceinline__ void store4(float* p, unsigned range, bool vec, const
     if ((range >> k & 1u) && store_allowed(p + k, 4, r, status)) p[k] = x[k];
 }
 
+// The top bit of each byte of w that is not 0.
+__device__ __forceinline__ unsigned nonzero_bytes(unsigned w) {
+  return (((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w) & 0x80808080u;
+}
+
 // Which of the tokens i .. i + 3 of the mask (of those in `range`) count.
 __device__ __forceinline__ unsigned mask4(const TokenView& t, long long i, unsigned range, bool vec) {
   if (t.mask_kind == FLCE_MASK_NONE) return range;
   unsigned bits = 0;
   if (t.mask_kind == FLCE_MASK_BYTES) {
     const unsigned char* m = static_cast<const unsigned char*>(t.mask) + i;
-    if (vec) {
-      const unsigned w = __vsetgtu4(__ldg(reinterpret_cast<const unsigned*>(m)), 0u);   // 1 a byte
-      return (w * 0x01020408u) >> 24;   // byte k to bit 24 + k, without carries
-    }
+    if (vec)   // bits 7, 15, 23, 31 to 28, 29, 30, 31, without carries
+      return (nonzero_bytes(__ldg(reinterpret_cast<const unsigned*>(m))) * 0x00204081u) >> 28;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (range >> k & 1u) bits |= (m[k] != 0 ? 1u : 0u) << k;
@@ -224,57 +227,144 @@ struct Group {
     }
     whole = rest >= 4;
     range = whole ? 15u : (1u << rest) - 1u;
-    unsigned in = range;
+    bits = mask4(t, index(t.ld_mask), range, a.vec_mask && whole);
     if (kFlat && t.cu != nullptr) {
       // tokens outside every sequence do not count
       const long long first = __ldg(t.cu), end = t.S > 0 ? __ldg(t.cu + t.S) : 0;
+      if (at < first || at + 4 > end) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (at + k < first || at + k >= end) in &= ~(1u << k);
+        for (int k = 0; k < 4; ++k)
+          if (at + k < first || at + k >= end) bits &= ~(1u << k);
+      }
     }
-    bits = mask4(t, index(t.ld_mask), range, a.vec_mask && whole) & in;
   }
 };
 
 // --------------------------------------------------------------- policy
-// The terms of one token, not yet weighted.
-struct Term {
-  float loss, grad, kl;
-  bool clipped;
+// What a thread adds up over its tokens: gains (minus the loss) and KL terms.
+struct Running {
+  Sum gain, kl;
+  int clipped, tokens;
 };
 
-__device__ __forceinline__ Term policy_term(const PolicyArgs& a, float x, float old, float ref,
-                                            float adv) {
-  Term o{0.f, 0.f, 0.f, false};
-  const float d = a.old != nullptr ? __fsub_rn(x, old) : 0.f;
-  const float r = expf(d);
-  const bool over = d > a.hi, under = d < a.lo;
-  // max(-A r, -A clipped r): the clip takes the term where it lowers the gain
-  o.clipped = (adv > 0.f && over) || (adv < 0.f && under);
-  o.loss = -adv * (o.clipped ? (over ? a.ratio_hi : a.ratio_lo) : r);
-  o.grad = o.clipped ? 0.f : -adv * r;
-  if (a.dual > 0.f && adv < 0.f && d > a.log_dual) {
-    o.loss = -a.dual * adv;
-    o.grad = 0.f;
-    o.clipped = true;
-  }
-  if (adv == 0.f && !isnan(d)) o.loss = o.grad = 0.f;   // not 0 x infinity
-  if (a.kl_coef != 0.f) {
-    const float e = __fsub_rn(x, ref);
-    float dkl = 1.f;
-    o.kl = e;
-    if (a.kl == FLCE_KL_K2) {
-      o.kl = 0.5f * e * e;
-      dkl = e;
-    } else if (a.kl == FLCE_KL_K3) {
-      const float q = expm1f(-e);
-      o.kl = q + e;
-      dkl = -q;
+__device__ __forceinline__ unsigned long long both(float x) { return f2pack(x, x); }
+
+// N tokens of log probs x, all of which count: the gain of each and its
+// derivative in the log prob, not yet weighted. KL terms and clipped tokens are
+// added to `v`. kKl: flce_kl, or -1 without a KL term.
+template <int kKl, int N>
+__device__ __forceinline__ void policy_terms(const PolicyArgs& a, const float (&x)[N],
+                                             const float (&old)[N], const float (&ref)[N],
+                                             const float (&adv)[N], float (&gain)[N],
+                                             float (&slope)[N], Running& v) {
+  constexpr float kLog2e = 1.44269504f;
+  float kl_sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const float d = fmaf(a.sign, x[k], -old[k]);
+    // min(A r, A clipped r): the clip takes the term where it lowers the gain,
+    // past the bound on the side of A's sign: where (d - bound) A > 0. (An
+    // infinite d is kept finite there, so that A = 0 makes it 0.)
+    const bool up = adv[k] > 0.f;
+    float past;
+    asm("min.NaN.f32 %0, %1, 0f7F7FFFFF;" : "=f"(past) : "f"(d - (up ? a.hi : a.lo)));
+    past *= adv[k];
+    float edge = up ? a.ratio_hi : a.ratio_lo;
+    bool clipped = past > 0.f;
+    if (a.dual > 0.f) {
+      const bool over = adv[k] < 0.f && d > a.log_dual;
+      edge = over ? a.dual : edge;
+      clipped = clipped || over;
     }
-    o.loss = fmaf(a.kl_coef, o.kl, o.loss);
-    o.grad = fmaf(a.kl_coef, dkl, o.grad);
+    v.clipped += clipped ? 1 : 0;
+    const bool flat = clipped || adv[k] == 0.f;   // 0, not 0 x infinity
+    const float g = adv[k] * ex2_approx(d * kLog2e);
+    gain[k] = flat ? adv[k] * edge : g;
+    slope[k] = flat ? 0.f : g;
   }
-  return o;
+  if (kKl >= 0) {
+    // Two tokens at a time in packed arithmetic, with u = ref - log prob.
+    // exp(u) - u - 1 cancels near 0; there it is u^2 times its Taylor series
+    // (to u^7 / 7!: what is left out is below 2^-24 of it for |u| < 0.4). Its
+    // derivative in the log prob is 1 - exp(u) = -(it + u) either way.
+#pragma unroll
+    for (int k = 0; k < N; k += 2) {
+      const unsigned long long uu = fma2(f2pack(x[k], x[k + 1]), both(-a.sign), f2pack(ref[k], ref[k + 1]));
+      unsigned long long kl, minus_slope;   // the KL term, and minus its derivative
+      if (kKl == FLCE_KL_K1) {
+        kl = mul2(uu, both(-1.f));
+        minus_slope = both(-1.f);
+      } else if (kKl == FLCE_KL_K2) {
+        kl = mul2(mul2(uu, uu), both(0.5f));
+        minus_slope = uu;
+      } else {
+        unsigned long long p = fma2(both(1.f / 5040.f), uu, both(1.f / 720.f));
+        p = fma2(p, uu, both(1.f / 120.f));
+        p = fma2(p, uu, both(1.f / 24.f));
+        p = fma2(p, uu, both(1.f / 6.f));
+        p = fma2(p, uu, both(0.5f));
+        float u[2], near[2], far[2], e[2];
+        f2unpack(uu, u[0], u[1]);
+        f2unpack(mul2(mul2(uu, uu), p), near[0], near[1]);
+        f2unpack(mul2(uu, both(kLog2e)), e[0], e[1]);
+        const unsigned long long q = add2(f2pack(ex2_approx(e[0]), ex2_approx(e[1])), both(-1.f));
+        f2unpack(fma2(uu, both(-1.f), q), far[0], far[1]);
+#pragma unroll
+        for (int o = 0; o < 2; ++o) near[o] = fabsf(u[o]) < 0.4f ? near[o] : far[o];
+        kl = f2pack(near[0], near[1]);
+        minus_slope = add2(kl, uu);
+      }
+      float t[2];
+      f2unpack(kl, t[0], t[1]);
+      kl_sum += t[0] + t[1];
+      f2unpack(fma2(kl, both(-a.kl_coef), f2pack(gain[k], gain[k + 1])), gain[k], gain[k + 1]);
+      f2unpack(fma2(minus_slope, both(a.kl_coef), f2pack(slope[k], slope[k + 1])), slope[k], slope[k + 1]);
+    }
+  }
+  if (kKl >= 0) v.kl.add(kl_sum);
+}
+template <int N>
+__device__ __forceinline__ void policy_tokens(const PolicyArgs& a, const float (&x)[N],
+                                              const float (&old)[N], const float (&ref)[N],
+                                              const float (&adv)[N], float (&gain)[N],
+                                              float (&slope)[N], Running& v) {
+  if (a.kl_coef == 0.f)
+    policy_terms<-1>(a, x, old, ref, adv, gain, slope, v);
+  else if (a.kl == FLCE_KL_K3)
+    policy_terms<FLCE_KL_K3>(a, x, old, ref, adv, gain, slope, v);
+  else if (a.kl == FLCE_KL_K2)
+    policy_terms<FLCE_KL_K2>(a, x, old, ref, adv, gain, slope, v);
+  else
+    policy_terms<FLCE_KL_K1>(a, x, old, ref, adv, gain, slope, v);
+}
+
+// A token that does not count goes through the arithmetic as one whose terms
+// are all 0 ...
+__device__ __forceinline__ void silence(bool on, float& x, float& old, float& ref, float& adv) {
+  x = on ? x : 0.f;
+  old = on ? old : 0.f;
+  ref = on ? ref : 0.f;
+  adv = on ? adv : 0.f;
+}
+// ... but for the slope of the KL estimator k1, which is 1 everywhere; its
+// gradient is dropped.
+
+// The tokens of `bits` of a group, each with its advantage and weight:
+// d loss / d log_probs in `out`.
+__device__ __forceinline__ void policy_group(const PolicyArgs& a, unsigned bits, float (&x)[4],
+                                             float (&old)[4], float (&ref)[4], float (&adv)[4],
+                                             const float (&weight)[4], float (&out)[4], Running& v) {
+  float gain[4], slope[4], sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) silence(bits >> k & 1u, x[k], old[k], ref[k], adv[k]);
+  policy_tokens(a, x, old, ref, adv, gain, slope, v);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    sum = fmaf(gain[k], weight[k], sum);
+    out[k] = bits >> k & 1u ? slope[k] * (-a.sign * weight[k]) : 0.f;
+  }
+  v.gain.add(sum);
+  v.tokens += __popc(bits);
 }
 
 template <typename T, bool kFlat>
@@ -282,21 +372,26 @@ __device__ __forceinline__ void policy_load(const PolicyArgs& a, const Group<kFl
                                             float (&old)[4], float (&ref)[4], float (&adv)[4]) {
   const bool vec = a.vec && g.whole;
   load4(static_cast<const T*>(a.lp) + g.index(a.ld_lp), g.bits, vec, x);
-  if (a.old != nullptr) load4(static_cast<const T*>(a.old) + g.index(a.ld_old), g.bits, vec, old);
+  if (a.old != nullptr) {
+    load4(static_cast<const T*>(a.old) + g.index(a.ld_old), g.bits, vec, old);
+  } else {   // the log ratio is 0
+#pragma unroll
+    for (int k = 0; k < 4; ++k) old[k] = a.sign * x[k];
+  }
   if (a.kl_coef != 0.f) load4(static_cast<const T*>(a.ref) + g.index(a.ld_ref), g.bits, vec, ref);
   if (a.adv_per_token) load4(a.adv + g.index(a.ld_adv), g.bits, vec, adv);
 }
 
 // What the reduced outputs are made of.
 struct Totals {
-  Sum loss, kl;
+  Sum gain, kl;
   long long clipped, tokens;
 };
 
 __device__ __forceinline__ void policy_outputs(const PolicyArgs& a, const Totals& v) {
   const bool none = (a.reduction == FLCE_TOKEN_MEAN && v.tokens == 0) ||
                     (a.reduction == FLCE_SEQUENCE_MEAN && a.t.S == 0);
-  *a.loss = none ? NAN : v.loss.total();
+  *a.loss = none ? NAN : 0.f - v.gain.total();
   if (a.num_tokens != nullptr) *a.num_tokens = v.tokens;
   if (a.num_clipped != nullptr) *a.num_clipped = v.clipped;
   if (a.kl_sum != nullptr) *a.kl_sum = v.kl.total();
@@ -324,88 +419,109 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads
   }
   const long long q = static_cast<long long>(blockIdx.x) * kSmallThreads + threadIdx.x;
   Group<kFlat> g{};
-  float x[4], old[4], ref[4], adv[4];
+  float x[4] = {}, old[4] = {}, ref[4] = {}, adv[4] = {}, weight[4] = {1.f, 1.f, 1.f, 1.f}, out[4] = {};
   if (q < a.groups) g.find(a, q);
   if (g.bits != 0) policy_load<T>(a, g, x, old, ref, adv);
-  int row[4];
-  Term term[4];
-  Walker w;
+  int row[4] = {};
+  if (by_sequence || !a.adv_per_token) {
+    Walker w;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    row[k] = 0;
-    term[k] = Term{0.f, 0.f, 0.f, false};
-    if (!(g.bits >> k & 1u)) continue;
-    if (by_sequence || !a.adv_per_token) {
+    for (int k = 0; k < 4; ++k) {
+      if (!(g.bits >> k & 1u)) continue;
       if (kFlat) w.to(a.t, g.at + k); else w.s = g.row;
       row[k] = static_cast<int>(w.s);
+      if (count_rows) atomicAdd(s_count + row[k], 1);
+      if (!a.adv_per_token) adv[k] = __ldg(a.adv + row[k]);
     }
-    if (count_rows) atomicAdd(s_count + row[k], 1);
-    term[k] = policy_term(a, a.sign * x[k], old[k], ref[k], a.adv_per_token ? adv[k] : a.adv[row[k]]);
   }
   const int n = block_total(__popc(g.bits));
   if (threadIdx.x == 0) s_totals.tokens = n;
   cluster.sync();
   long long tokens = 0;
   for (int b = 0; b < kCluster; ++b) tokens += cluster.map_shared_rank(&s_totals, b)->tokens;
-  float weight = a.reduction == FLCE_TOKEN_MEAN ? 1.f / static_cast<float>(tokens) : 1.f;
-  Sum loss{}, kl{};
-  int clipped = 0;
-  float out[4];
-  int have = -1;
+  if (a.reduction == FLCE_TOKEN_MEAN) {
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    out[k] = 0.f;
-    if (!(g.bits >> k & 1u)) continue;
-    if (by_sequence && row[k] != have) {
-      have = row[k];
-      long long c = 0;
-      if (count_rows)
-        for (int b = 0; b < kCluster; ++b) c += *cluster.map_shared_rank(s_count + have, b);
-      else
-        c = sequence_end(a.t, have, sequence_first(a.t, have)) - sequence_first(a.t, have);
-      weight = sequence_weight(a, c);
+    for (int k = 0; k < 4; ++k) weight[k] = 1.f / static_cast<float>(tokens);
+  } else if (by_sequence) {
+    int have = -1;
+    float w = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (!(g.bits >> k & 1u)) continue;
+      if (row[k] != have) {
+        have = row[k];
+        long long c = 0;
+        if (count_rows)
+          for (int b = 0; b < kCluster; ++b) c += *cluster.map_shared_rank(s_count + have, b);
+        else
+          c = sequence_end(a.t, have, sequence_first(a.t, have)) - sequence_first(a.t, have);
+        w = sequence_weight(a, c);
+      }
+      weight[k] = w;
     }
-    out[k] = term[k].grad * weight * a.sign;
-    loss.add(term[k].loss * weight);
-    kl.add(term[k].kl);
-    clipped += term[k].clipped ? 1 : 0;
   }
+  Running v{};
+  if (g.bits != 0) policy_group(a, g.bits, x, old, ref, adv, weight, out, v);
   if (a.grad != nullptr && q < a.groups)
     store4(a.grad + g.index(a.ld_grad), g.range, a.vec_grad && g.whole, out, a.r_grad, a.status);
-  loss = block_total(loss);
-  kl = block_total(kl);
-  clipped = block_total(clipped);
+  v.gain = block_total(v.gain);
+  v.kl = block_total(v.kl);
+  v.clipped = block_total(v.clipped);
   if (threadIdx.x == 0) {
-    s_totals.loss = loss;
-    s_totals.kl = kl;
-    s_totals.clipped = clipped;
+    s_totals.gain = v.gain;
+    s_totals.kl = v.kl;
+    s_totals.clipped = v.clipped;
   }
   cluster.sync();
   if (cluster.block_rank() == 0 && threadIdx.x == 0) {
-    Totals v{};
+    Totals all{};
     for (int b = 0; b < kCluster; ++b) {
       const Totals* o = cluster.map_shared_rank(&s_totals, b);
-      v.loss = v.loss + o->loss;
-      v.kl = v.kl + o->kl;
-      v.clipped += o->clipped;
+      all.gain = all.gain + o->gain;
+      all.kl = all.kl + o->kl;
+      all.clipped += o->clipped;
     }
-    v.tokens = tokens;
-    policy_outputs(a, v);
+    all.tokens = tokens;
+    policy_outputs(a, all);
   }
   cluster.sync();   // the other blocks' shared memory stays until it has been read
 }
 
-// Tokens that count, one number a block ("mean").
+// Tokens that count, one number a block ("mean"). Of a contiguous byte mask
+// 16 tokens a thread and step; the bytes before and behind the aligned ones
+// are block 0's.
 template <bool kFlat>
 __global__ void __launch_bounds__(kThreads) count_tokens_kernel(const PolicyArgs a) {
   allow_next();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
   int n = 0;
   const long long step = static_cast<long long>(gridDim.x) * kThreads;
-  for (long long q = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x; q < a.groups; q += step) {
-    Group<kFlat> g;
-    g.find(a, q);
-    n += __popc(g.bits);
+  const long long me = static_cast<long long>(blockIdx.x) * kThreads + threadIdx.x;
+  if (kFlat && a.t.mask_kind == FLCE_MASK_BYTES) {
+    const unsigned char* m = static_cast<const unsigned char*>(a.t.mask);
+    const long long first = a.t.cu != nullptr ? sequence_first(a.t, 0) : 0;
+    const long long end = a.t.cu != nullptr ? max(first, a.t.S > 0 ? sequence_first(a.t, a.t.S) : 0) : a.t.N;
+    const long long off = static_cast<long long>(reinterpret_cast<uintptr_t>(m + first) & 15u);
+    const long long from = min(end, first + (off == 0 ? 0 : 16 - off)), vectors = (end - from) / 16;
+    const uint4* v = reinterpret_cast<const uint4*>(m + from);
+#pragma unroll 4
+    for (long long i = me; i < vectors; i += step) {
+      const uint4 w = __ldg(v + i);
+      // one bit a byte, moved apart, so that one population count does for all four
+      n += __popc(nonzero_bytes(w.x) | nonzero_bytes(w.y) >> 1 | nonzero_bytes(w.z) >> 2 |
+                  nonzero_bytes(w.w) >> 3);
+    }
+    if (blockIdx.x == 0) {
+      const long long behind = from + vectors * 16;
+      if (threadIdx.x < from - first) n += m[first + threadIdx.x] != 0 ? 1 : 0;
+      if (threadIdx.x < end - behind) n += m[behind + threadIdx.x] != 0 ? 1 : 0;
+    }
+  } else {
+    for (long long q = me; q < a.groups; q += step) {
+      Group<kFlat> g;
+      g.find(a, q);
+      n += __popc(g.bits);
+    }
   }
   const long long total = block_total(static_cast<long long>(n));
   if (threadIdx.x == 0 && store_allowed(a.counts + blockIdx.x, 8, a.r_ws, a.status))
@@ -443,199 +559,498 @@ __global__ void __launch_bounds__(kThreads) count_sequences_kernel(const PolicyA
   }
 }
 
-// a.per groups a block, kThreads at a time; the mask of the next ones is on
-// its way while these are computed.
+// The weight of a token under "sum" and "mean", and the batch's tokens that
+// count ("mean" only).
+__device__ __forceinline__ float batch_weight(const PolicyArgs& a) {
+  if (a.reduction != FLCE_TOKEN_MEAN) return 1.f;
+  long long tokens = 0;
+  if (a.num_counts > 0) {
+    for (int i = threadIdx.x; i < a.num_counts; i += kThreads) tokens += a.counts[i];
+    tokens = block_total(tokens);
+  } else {   // without a mask: what lies in sequences
+    tokens = a.t.cu == nullptr ? a.t.N
+             : a.t.S > 0 ? max(0ll, clamp_to(a.t.cu[a.t.S], a.t.N) - clamp_to(a.t.cu[0], a.t.N)) : 0;
+  }
+  return 1.f / static_cast<float>(tokens);
+}
+
+// The sequence that a thread is in: its advantage and weight.
+struct Sequence {
+  Walker w;
+  long long have = -1;
+  float adv = 0.f, weight;
+  __device__ __forceinline__ explicit Sequence(float batch) : weight(batch) {}
+  __device__ __forceinline__ void enter(const PolicyArgs& a) {
+    if (w.s == have) return;
+    have = w.s;
+    if (!a.adv_per_token) adv = __ldg(a.adv + have);
+    if (a.reduction == FLCE_SEQUENCE_MEAN) {
+      const long long first = sequence_first(a.t, have);
+      weight = sequence_weight(a, a.num_counts > 0 ? a.counts[have]
+                                                   : sequence_end(a.t, have, first) - first);
+    }
+  }
+};
+
+// A block's share of the outputs; the last block to finish adds them up.
+__device__ __forceinline__ void policy_finish(const PolicyArgs& a, Running& v) {
+  v.gain = block_total(v.gain);
+  v.kl = block_total(v.kl);
+  const long long both = block_total(static_cast<long long>(v.clipped) << 32 |
+                                     static_cast<long long>(v.tokens));
+  __shared__ bool s_last;
+  if (threadIdx.x == 0) {
+    if (store_allowed(a.partials + blockIdx.x, sizeof(PolicyPartial), a.r_ws, a.status))
+      a.partials[blockIdx.x] = PolicyPartial{v.gain.s, v.gain.c, v.kl.s, v.kl.c, both};
+    s_last = counted_last(a.done, static_cast<int>(gridDim.x));
+  }
+  __syncthreads();
+  if (!s_last) return;
+  Totals all{};
+  for (unsigned b = threadIdx.x; b < gridDim.x; b += kThreads) {
+    const PolicyPartial* o = a.partials + b;
+    const float4 f = __ldcg(reinterpret_cast<const float4*>(o));
+    const long long n = __ldcg(&o->both);
+    all.gain = all.gain + Sum{f.x, f.y};
+    all.kl = all.kl + Sum{f.z, f.w};
+    all.clipped += n >> 32;
+    all.tokens += n & 0xffffffffll;
+  }
+  all.gain = block_total(all.gain);
+  all.kl = block_total(all.kl);
+  all.clipped = block_total(all.clipped);
+  all.tokens = block_total(all.tokens);
+  if (threadIdx.x == 0) policy_outputs(a, all);
+}
+
+// The streaming kernel of strided and of unaligned batches: a.per groups of
+// four a block, kThreads at a time; the mask of the next ones is on its way
+// while these are computed.
 template <typename T, bool kFlat>
-__global__ void __launch_bounds__(kThreads, kPolicyBlocksPerSm) policy_kernel(const PolicyArgs a) {
-  const bool by_sequence = a.reduction == FLCE_SEQUENCE_MEAN;
-  const bool need_row = by_sequence || !a.adv_per_token;
+__global__ void __launch_bounds__(kThreads) policy_kernel(const PolicyArgs a) {
+  const bool need_row = a.reduction == FLCE_SEQUENCE_MEAN || !a.adv_per_token;
   long long q = blockIdx.x * a.per + threadIdx.x;
   const long long end = min(a.groups, (blockIdx.x + 1) * a.per);
   Group<kFlat> g{}, next{};
   if (q < end) next.find(a, q);
   wait_for_previous();
-  long long tokens = 0;
-  float weight = 1.f;
-  if (a.reduction == FLCE_TOKEN_MEAN) {
-    if (a.num_counts > 0) {
-      for (int i = threadIdx.x; i < a.num_counts; i += kThreads) tokens += a.counts[i];
-      tokens = block_total(tokens);
-    } else {   // without a mask: what lies in sequences
-      tokens = a.t.cu == nullptr ? a.t.N
-               : a.t.S > 0 ? max(0ll, clamp_to(a.t.cu[a.t.S], a.t.N) - clamp_to(a.t.cu[0], a.t.N)) : 0;
-    }
-    weight = 1.f / static_cast<float>(tokens);
-  }
-  Sum loss{}, kl{};
-  int clipped = 0, seen = 0;
-  Walker w;
-  long long have = -1;
-  float adv_row = 0.f;
+  Sequence seq(batch_weight(a));
+  Running v{};
   for (; q < end; q += kThreads) {
     g = next;
     if (q + kThreads < end) next.find(a, q + kThreads);
-    float out[4] = {0.f, 0.f, 0.f, 0.f};
+    float out[4] = {};
     if (g.bits != 0) {
-      float x[4], old[4], ref[4], adv[4];
+      float x[4], old[4], ref[4] = {}, adv[4], weights[4];
       policy_load<T>(a, g, x, old, ref, adv);
-      float l = 0.f, kk = 0.f;
+      if (!kFlat) seq.w.s = g.row;
+      if (!kFlat && need_row) seq.enter(a);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        if (!(g.bits >> k & 1u)) continue;
-        if (need_row) {
-          if (kFlat) w.to(a.t, g.at + k); else w.s = g.row;
-          if (w.s != have) {
-            have = w.s;
-            if (!a.adv_per_token) adv_row = __ldg(a.adv + have);
-            if (by_sequence) {
-              const long long first = sequence_first(a.t, have);
-              weight = sequence_weight(a, a.num_counts > 0 ? a.counts[have]
-                                                           : sequence_end(a.t, have, first) - first);
-            }
-          }
+        if (kFlat && need_row && (g.bits >> k & 1u)) {
+          seq.w.to(a.t, g.at + k);
+          seq.enter(a);
         }
-        const Term o = policy_term(a, a.sign * x[k], old[k], ref[k], a.adv_per_token ? adv[k] : adv_row);
-        out[k] = o.grad * weight * a.sign;
-        l += o.loss * weight;
-        kk += o.kl;
-        clipped += o.clipped ? 1 : 0;
+        if (!a.adv_per_token) adv[k] = seq.adv;
+        weights[k] = seq.weight;
       }
-      loss.add(l);
-      kl.add(kk);
-      seen += __popc(g.bits);
+      policy_group(a, g.bits, x, old, ref, adv, weights, out, v);
     }
     if (a.grad != nullptr)
       store4(a.grad + g.index(a.ld_grad), g.range, a.vec_grad && g.whole, out, a.r_grad, a.status);
   }
-  loss = block_total(loss);
-  kl = block_total(kl);
-  const long long both = block_total(static_cast<long long>(clipped) << 32 | static_cast<long long>(seen));
-  if (threadIdx.x == 0 && store_allowed(a.partials + blockIdx.x, sizeof(PolicyPartial), a.r_ws, a.status))
-    a.partials[blockIdx.x] = PolicyPartial{loss.s, loss.c, kl.s, kl.c, both};
-  if (!last_block(a.done)) return;
-  Totals v{};
-  for (unsigned i = threadIdx.x; i < gridDim.x; i += kThreads) {
-    const PolicyPartial* o = a.partials + i;
-    const float4 f = __ldcg(reinterpret_cast<const float4*>(o));
-    const long long n = __ldcg(&o->both);
-    v.loss = v.loss + Sum{f.x, f.y};
-    v.kl = v.kl + Sum{f.z, f.w};
-    v.clipped += n >> 32;
-    v.tokens += n & 0xffffffffll;
+  policy_finish(a, v);
+}
+
+// ------------------------------------------------------- octets of tokens
+// Eight neighbouring tokens. In a set of them, bit 2t stands for token t < 4
+// and bit 2 (t - 4) + 1 for token t >= 4, which is how eight mask bytes fold
+// into one.
+constexpr unsigned kWhole = 0xffu;
+__device__ __forceinline__ constexpr int bit_of(int t) { return t < 4 ? 2 * t : 2 * t - 7; }
+__device__ __forceinline__ bool has(unsigned set, int t) { return set >> bit_of(t) & 1u; }
+__device__ __forceinline__ unsigned tokens_from_to(int from, int to) {
+  unsigned r = 0;
+#pragma unroll
+  for (int t = 0; t < 8; ++t) r |= (t >= from && t < to ? 1u : 0u) << bit_of(t);
+  return r;
+}
+// The bytes of w that are not 0. The top bits of the upper word and, moved down
+// by one, of the lower word make bit pairs, which the product gathers.
+__device__ __forceinline__ unsigned nonzero_set(uint2 w) {
+  return ((nonzero_bytes(w.x) >> 1 | nonzero_bytes(w.y)) * 0x00041041u) >> 24;
+}
+__device__ __forceinline__ unsigned mask8(const TokenView& t, long long i, unsigned range, bool vec) {
+  if (t.mask_kind == FLCE_MASK_NONE) return range;
+  unsigned set = 0;
+  if (t.mask_kind == FLCE_MASK_BYTES) {
+    const unsigned char* m = static_cast<const unsigned char*>(t.mask) + i;
+    if (vec) return nonzero_set(__ldg(reinterpret_cast<const uint2*>(m)));
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (has(range, k)) set |= (m[k] != 0 ? 1u : 0u) << bit_of(k);
+    return set;
   }
-  v.loss = block_total(v.loss);
-  v.kl = block_total(v.kl);
-  v.clipped = block_total(v.clipped);
-  v.tokens = block_total(v.tokens);
-  if (threadIdx.x == 0) policy_outputs(a, v);
+  const long long* m = static_cast<const long long*>(t.mask) + i;
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (has(range, k)) set |= (__ldg(m + k) != t.ignore_index ? 1u : 0u) << bit_of(k);
+  return set;
+}
+// The tokens of `set`; the others read as 0 (or, with kVec, as they are).
+template <bool kVec, typename T>
+__device__ __forceinline__ void load_octet(const T* p, unsigned set, float (&x)[8]) {
+  if (kVec) {
+    load8(p, x);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) x[k] = has(set, k) ? to_f32(p[k]) : 0.f;
+}
+template <bool kVec>
+__device__ __forceinline__ void store_octet(float* p, unsigned range, const float (&x)[8], const DevRegion& r,
+                                            int* status) {
+  if (kVec) {
+    if (store_allowed(p, 32, r, status)) store8(p, x);
+    return;
+  }
+#pragma unroll
+  for (int k = 0; k < 8; ++k)
+    if (has(range, k) && store_allowed(p + k, 4, r, status)) p[k] = x[k];
+}
+
+// One octet of the contiguous streaming kernel: `set` of it counts, `range`
+// exists, p* point at it. `at` is its flat token.
+template <typename T, bool kVec>
+__device__ __forceinline__ void policy_octet(const PolicyArgs& a, long long at, unsigned set, unsigned range,
+                                             Sequence& seq, Running& v) {
+  float out[8] = {};
+  if (set != 0) {
+    float x[8], old[8], ref[8] = {}, adv[8], gain[8], slope[8], sum = 0.f;
+    load_octet<kVec>(static_cast<const T*>(a.lp) + at, set, x);
+    if (a.old != nullptr) load_octet<kVec>(static_cast<const T*>(a.old) + at, set, old);
+    if (a.kl_coef != 0.f) load_octet<kVec>(static_cast<const T*>(a.ref) + at, set, ref);
+    if (a.adv_per_token) load_octet<kVec>(a.adv + at, set, adv);
+    if (a.old == nullptr) {   // the log ratio is 0
+#pragma unroll
+      for (int k = 0; k < 8; ++k) old[k] = a.sign * x[k];
+    }
+    const bool need_row = a.reduction == FLCE_SEQUENCE_MEAN || !a.adv_per_token;
+    const bool several = need_row && at + 7 >= seq.w.end;   // perhaps several sequences
+    Sequence again = seq;
+    if (!a.adv_per_token) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) adv[k] = seq.adv;
+      if (several) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          if (!has(set, k)) continue;
+          seq.w.to(a.t, at + k);
+          seq.enter(a);
+          adv[k] = seq.adv;
+        }
+      }
+    }
+    if (set != kWhole) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) silence(has(set, k), x[k], old[k], ref[k], adv[k]);
+    }
+    policy_tokens(a, x, old, ref, adv, gain, slope, v);
+    v.tokens += __popc(set);
+    if (several && a.reduction == FLCE_SEQUENCE_MEAN) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        if (!has(set, k)) continue;
+        again.w.to(a.t, at + k);
+        again.enter(a);
+        sum = fmaf(gain[k], again.weight, sum);
+        out[k] = slope[k] * (-a.sign * again.weight);
+      }
+      seq = again;
+    } else {
+      const float w = -a.sign * seq.weight;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        sum += gain[k];
+        out[k] = slope[k] * w;
+      }
+      sum *= seq.weight;
+      if (set != kWhole) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) out[k] = has(set, k) ? out[k] : 0.f;
+      }
+    }
+    v.gain.add(sum);
+  }
+  if (a.grad != nullptr) store_octet<kVec>(a.grad + at, range, out, a.r_grad, a.status);
+}
+
+// The streaming kernel of contiguous, aligned batches: a.per octets a block,
+// kThreads at a time, the masks of the next ones on their way; the last few
+// tokens are the last block's.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, kPolicyBlocksPerSm) policy_octets_kernel(const PolicyArgs a) {
+  const long long octets = a.t.N / 8, o0 = blockIdx.x * a.per;
+  const int count = static_cast<int>(min(octets - o0, a.per));
+  const bool masked = a.t.mask_kind != FLCE_MASK_NONE;
+  int i = threadIdx.x;
+  unsigned next = kWhole;
+  if (masked && i < count) next = mask8(a.t, (o0 + i) * 8, kWhole, true);
+  // the tokens that lie in sequences
+  long long first = 0, end = a.t.N;
+  if (a.t.cu != nullptr) {
+    first = clamp_to(__ldg(a.t.cu), a.t.N);
+    end = a.t.S > 0 ? clamp_to(__ldg(a.t.cu + a.t.S), a.t.N) : 0;
+  }
+  const bool inside = first <= o0 * 8 && (o0 + count) * 8 <= end;   // all of the block's
+  wait_for_previous();
+  Sequence seq(batch_weight(a));
+  Running v{};
+  for (; i < count; i += kThreads) {
+    unsigned set = next;
+    if (masked && i + kThreads < count) next = mask8(a.t, (o0 + i + kThreads) * 8, kWhole, true);
+    const long long at = (o0 + i) * 8;
+    if (!inside)
+      set &= tokens_from_to(static_cast<int>(min(max(first - at, 0ll), 8ll)),
+                            static_cast<int>(min(max(end - at, 0ll), 8ll)));
+    policy_octet<T, true>(a, at, set, kWhole, seq, v);
+  }
+  const int tail = static_cast<int>(a.t.N - octets * 8);
+  if (tail != 0 && blockIdx.x == gridDim.x - 1 && threadIdx.x == kThreads - 1) {
+    const long long at = octets * 8;
+    const unsigned range = tokens_from_to(0, tail);
+    const unsigned set = mask8(a.t, at, range, false) &
+                         tokens_from_to(static_cast<int>(min(max(first - at, 0ll), 8ll)),
+                                        static_cast<int>(min(max(end - at, 0ll), 8ll)));
+    policy_octet<T, false>(a, at, set, range, seq, v);
+  }
+  policy_finish(a, v);
 }
 
 // ------------------------------------------------------------ preference
-// The tokens of one sequence, as the groups of four that a team of threads
-// goes through: group j of the sequence is tokens 4j - shift .. + 3, so that
-// the groups of a contiguous batch are aligned wherever the sequence begins.
+// One sequence as the octets that a team of threads goes through: octet q holds
+// tokens 8q - shift .. + 7, so that the octets of a contiguous batch are
+// aligned wherever the sequence begins. `lp` .. `grad` point at octet 0, which
+// `shift` tokens of an earlier sequence are part of. Octets [from, to) are
+// whole.
+template <typename T>
 struct Row {
-  long long first, len;   // flat token of the start; tokens
-  long long shift;
+  const T* lp;
+  const T* ref;
+  float* grad;
+  long long mask;            // offset of octet 0
+  int shift, len, octets, from, to;
   __device__ __forceinline__ void find(const PreferenceArgs& a, long long s) {
-    first = sequence_first(a.t, s);
-    len = sequence_end(a.t, s, first) - first;
-    shift = a.flat ? first & 3 : 0;
+    const long long at = sequence_first(a.t, s);
+    len = static_cast<int>(sequence_end(a.t, s, at) - at);
+    shift = a.flat ? static_cast<int>(at & 7) : 0;
+    lp = static_cast<const T*>(a.lp) + (a.flat ? at : s * a.ld_lp) - shift;
+    ref = static_cast<const T*>(a.ref) + (a.flat ? at : s * a.ld_ref) - shift;
+    grad = a.grad + (a.flat ? at : s * a.ld_grad) - shift;
+    mask = (a.flat ? at : s * a.t.ld_mask) - shift;
+    octets = len == 0 ? 0 : (len + shift + 7) >> 3;
+    from = shift == 0 ? 0 : 1;
+    to = max(from, (len + shift) >> 3);
+    if (octets == 0) from = to = 0;
   }
-  __device__ __forceinline__ long long groups() const { return (len + shift + 3) / 4; }
-  __device__ __forceinline__ unsigned range(long long c) const {
-    unsigned r = 15u;
-    if (c < 0) r = 15u << -c & 15u;
-    if (len - c < 4) r &= (1u << (len - c)) - 1u;
-    return r;
+  __device__ __forceinline__ unsigned range(int q) const {
+    return tokens_from_to(max(0, shift - 8 * q), min(8, len + shift - 8 * q));
+  }
+  template <bool kVec>
+  __device__ __forceinline__ float sum(const PreferenceArgs& a, int q, unsigned set) const {
+    float x[8], r[8], d = 0.f;
+    load_octet<kVec>(lp + 8ll * q, set, x);
+    if (a.ref != nullptr) {
+      load_octet<kVec>(ref + 8ll * q, set, r);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) r[k] = 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = fmaf(a.sign, x[k], -r[k]);
+    if (set != kWhole) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = has(set, k) ? x[k] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) d += x[k];
+    return d;
+  }
+  template <bool kVec>
+  __device__ __forceinline__ void write(const PreferenceArgs& a, int q, unsigned range, unsigned set,
+                                        float w) const {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = has(set, k) ? w : 0.f;
+    store_octet<kVec>(grad + 8ll * q, range, v, a.r_grad, a.status);
   }
 };
 
-constexpr int kKept = 16;   // groups of a thread whose mask stays in a register
+constexpr int kKept = 8;    // octets of a thread whose tokens that count stay in a register
+constexpr int kBatch = 2;   // octets that a thread reads at once
+
+// The sums and token counts of a pair's two sequences, of a warp, a block or
+// the whole team.
+struct PairPart {
+  float c, r;
+  int n_c, n_r;
+};
+__device__ __forceinline__ PairPart warp_sum(PairPart v) {
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) {
+    v.c += __shfl_xor_sync(0xffffffffu, v.c, o);
+    v.r += __shfl_xor_sync(0xffffffffu, v.r, o);
+  }
+  v.n_c = __reduce_add_sync(0xffffffffu, v.n_c);
+  v.n_r = __reduce_add_sync(0xffffffffu, v.n_r);
+  return v;
+}
+
+// A team that is one block, and one that is a cluster.
+struct BlockTeam {
+  __device__ __forceinline__ void operator()(PairPart&) const { __syncwarp(); }
+  __device__ __forceinline__ PairPart get(const PairPart& own) const { return own; }
+};
+struct ClusterTeam {
+  __device__ __forceinline__ void operator()(PairPart&) const { cg::this_cluster().sync(); }
+  __device__ __forceinline__ PairPart get(PairPart& own) const {
+    cg::cluster_group cluster = cg::this_cluster();
+    PairPart v{};
+    for (unsigned i = 0; i < cluster.num_blocks(); ++i) {
+      const PairPart* o = cluster.map_shared_rank(&own, i);
+      v.c += o->c;
+      v.r += o->r;
+      v.n_c += o->n_c;
+      v.n_r += o->n_r;
+    }
+    return v;
+  }
+};
 
 // Both sequences of pair b by `team` threads, of which this is number
-// `member`. `total` adds a value over the team. Returns the pair's loss.
-template <typename T, class Total>
+// `member`. Returns the pair's loss. kVec: octets are aligned in every
+// tensor.
+template <typename T, bool kVec, class Total>
 __device__ __forceinline__ float preference_pair(const PreferenceArgs& a, long long b, int member,
-                                                  int team, Total total) {
+                                                 int team, Total total) {
   const long long pairs = a.t.S / 2;
+  const bool masked = a.t.mask_kind != FLCE_MASK_NONE;
+  Row<T> chosen, rejected;
+  chosen.find(a, b);
+  rejected.find(a, pairs + b);
+  // the whole octets of both sequences, one after the other
+  const int split = chosen.to - chosen.from, whole = split + rejected.to - rejected.from;
+  const auto row_of = [&](int k) { return k < split ? chosen : rejected; };
+  const auto octet_of = [&](int k) { return k < split ? k + chosen.from : k - split + rejected.from; };
   unsigned long long kept = 0;
-  int j = 0, n[2] = {0, 0};
-  Sum sum[2] = {};
-  Row row;
+  int index = 0, n_c = 0, n_r = 0;
+  Sum sum_c{}, sum_r{};
+  for (int j = member; j < whole; j += kBatch * team, index += kBatch) {
+    unsigned set[kBatch];
+    float d[kBatch];
 #pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const long long s = side == 0 ? b : pairs + b;
-    row.find(a, s);
-    const long long at_lp = a.flat ? row.first : s * a.ld_lp, at_ref = a.flat ? row.first : s * a.ld_ref;
-    const long long at_mask = a.flat ? row.first : s * a.t.ld_mask;
-    const long long groups = row.groups();
-    for (long long q = member; q < groups; q += team, ++j) {
-      const long long c = 4 * q - row.shift;
-      const unsigned range = row.range(c);
-      const unsigned bits = mask4(a.t, at_mask + c, range, a.vec_mask && range == 15u);
-      if (j < kKept) kept |= static_cast<unsigned long long>(bits) << (4 * j);
-      if (bits == 0) continue;
-      float x[4], r[4];
-      load4(static_cast<const T*>(a.lp) + at_lp + c, bits, a.vec && range == 15u, x);
-      if (a.ref != nullptr)
-        load4(static_cast<const T*>(a.ref) + at_ref + c, bits, a.vec && range == 15u, r);
-      float d = 0.f;
+    for (int i = 0; i < kBatch; ++i) {
+      const int k = j + i * team;
+      set[i] = k >= whole ? 0u
+               : masked ? mask8(a.t, row_of(k).mask + 8ll * octet_of(k), kWhole, kVec) : kWhole;
+      if (index + i < kKept) kept |= static_cast<unsigned long long>(set[i]) << (8 * (index + i));
+    }
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        if (bits >> k & 1u) d += a.ref != nullptr ? a.sign * x[k] - r[k] : a.sign * x[k];
-      sum[side].add(d);
-      n[side] += __popc(bits);
+    for (int i = 0; i < kBatch; ++i) {
+      const int k = j + i * team;
+      d[i] = set[i] != 0 ? row_of(k).template sum<kVec>(a, octet_of(k), set[i]) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const bool first = j + i * team < split;
+      const int count = __popc(set[i]);
+      sum_c.add(first ? d[i] : 0.f);
+      sum_r.add(first ? 0.f : d[i]);
+      n_c += first ? count : 0;
+      n_r += first ? 0 : count;
     }
   }
-  long long count = static_cast<long long>(n[0]) << 32 | static_cast<long long>(n[1]);
-  total(sum[0], sum[1], count);
-  float inv_c = 1.f, inv_r = 1.f;
-  if (a.average) {
-    inv_c = 1.f / static_cast<float>(max(1ll, count >> 32));
-    inv_r = 1.f / static_cast<float>(max(1ll, count & 0xffffffffll));
+  // Octets that are not whole: the first and the last of either sequence, the
+  // first four members'.
+  int edge = -1;
+  const bool side_c = member < 2;
+  const Row<T> own = side_c ? chosen : rejected;
+  if (member < 4) {
+    if ((member & 1) == 0 && own.from == 1) edge = 0;
+    if ((member & 1) == 1 && own.to < own.octets && !(own.from == 1 && own.octets == 1)) edge = own.to;
   }
-  const float s_c = sum[0].total() * inv_c, s_r = sum[1].total() * inv_r;
-  const float e = a.smoothing, z = a.beta * (s_c - s_r) - a.margin;
-  float loss, dz;
-  if (a.type == FLCE_PREF_SIGMOID) {
-    const float soft = log1pf(expf(-fabsf(z)));
-    loss = isnan(z) ? z : (1.f - e) * (soft + fmaxf(-z, 0.f)) + e * (soft + fmaxf(z, 0.f));
-    dz = e - 1.f / (1.f + expf(z));
-  } else if (a.type == FLCE_PREF_HINGE) {
-    loss = isnan(z) ? z : fmaxf(0.f, 1.f - z);
-    dz = z < 1.f ? -1.f : 0.f;
-  } else {
-    const float u = (z - 0.5f) / a.beta;
-    loss = u * u;
-    dz = 2.f * u / a.beta;
+  unsigned edge_set = 0;
+  if (edge >= 0) {
+    edge_set = mask8(a.t, own.mask + 8ll * edge, own.range(edge), false);
+    const float d = own.template sum<false>(a, edge, edge_set);
+    sum_c.add(side_c ? d : 0.f);
+    sum_r.add(side_c ? 0.f : d);
+    n_c += side_c ? __popc(edge_set) : 0;
+    n_r += side_c ? 0 : __popc(edge_set);
   }
-  if (member == 0) {
-    if (a.chosen != nullptr) a.chosen[b] = a.beta * s_c;
-    if (a.rejected != nullptr) a.rejected[b] = a.beta * s_r;
+  // Sums and counts over the team. Warps first, then the first warp of a block
+  // over its warps, which also does the pair's arithmetic: with every warp
+  // doing all of it, it was most of the instructions of a batch of 8192 a row.
+  __shared__ PairPart s_warp[kPairThreads / 32];
+  __shared__ PairPart s_block;
+  __shared__ float s_out[3];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  PairPart part{sum_c.total(), sum_r.total(), n_c, n_r};
+  part = warp_sum(part);
+  if (lane == 0) s_warp[warp] = part;
+  __syncthreads();
+  if (warp == 0) {
+    part = warp_sum(lane < kPairThreads / 32 ? s_warp[lane] : PairPart{});
+    if (lane == 0) s_block = part;
   }
+  total(s_block);
+  if (warp == 0) {
+    const PairPart p = total.get(s_block);
+    float inv_c = 1.f, inv_r = 1.f;
+    if (a.average) {
+      inv_c = 1.f / static_cast<float>(max(1, p.n_c));
+      inv_r = 1.f / static_cast<float>(max(1, p.n_r));
+    }
+    const float s_c = p.c * inv_c, s_r = p.r * inv_r;
+    const float e = a.smoothing, z = a.beta * (s_c - s_r) - a.margin;
+    float loss, dz;
+    if (a.type == FLCE_PREF_SIGMOID) {
+      const float soft = log1pf(expf(-fabsf(z)));
+      loss = isnan(z) ? z : (1.f - e) * (soft + fmaxf(-z, 0.f)) + e * (soft + fmaxf(z, 0.f));
+      dz = e - 1.f / (1.f + expf(z));
+    } else if (a.type == FLCE_PREF_HINGE) {
+      loss = isnan(z) ? z : fmaxf(0.f, 1.f - z);
+      dz = z < 1.f ? -1.f : 0.f;
+    } else {
+      const float u = (z - 0.5f) / a.beta;
+      loss = u * u;
+      dz = 2.f * u / a.beta;
+    }
+    if (member == 0) {
+      if (a.chosen != nullptr) a.chosen[b] = a.beta * s_c;
+      if (a.rejected != nullptr) a.rejected[b] = a.beta * s_r;
+    }
+    const float g = a.sign * a.beta * dz / static_cast<float>(pairs);
+    if (lane == 0) {
+      s_out[0] = g * inv_c;
+      s_out[1] = -g * inv_r;
+      s_out[2] = loss;
+    }
+  }
+  __syncthreads();
+  const float w_c = s_out[0], w_r = s_out[1], loss = s_out[2];
   if (a.grad == nullptr) return loss;
-  const float g = a.sign * a.beta * dz / static_cast<float>(pairs);
-  j = 0;
-#pragma unroll
-  for (int side = 0; side < 2; ++side) {
-    const long long s = side == 0 ? b : pairs + b;
-    row.find(a, s);
-    const float w = side == 0 ? g * inv_c : -g * inv_r;
-    const long long at_mask = a.flat ? row.first : s * a.t.ld_mask;
-    float* const out = a.grad + (a.flat ? row.first : s * a.ld_grad);
-    const long long groups = row.groups();
-    for (long long q = member; q < groups; q += team, ++j) {
-      const long long c = 4 * q - row.shift;
-      const unsigned range = row.range(c);
-      const unsigned bits = j < kKept ? static_cast<unsigned>(kept >> (4 * j)) & 15u
-                                      : mask4(a.t, at_mask + c, range, a.vec_mask && range == 15u);
-      float v[4];
-#pragma unroll
-      for (int k = 0; k < 4; ++k) v[k] = bits >> k & 1u ? w : 0.f;
-      store4(out + c, range, a.vec_grad && range == 15u, v, a.r_grad, a.status);
-    }
+  index = 0;
+  for (int k = member; k < whole; k += team, ++index) {
+    const Row<T> r = row_of(k);
+    const int q = octet_of(k);
+    unsigned set = kWhole;
+    if (masked)
+      set = index < kKept ? static_cast<unsigned>(kept >> (8 * index)) & kWhole
+                          : mask8(a.t, r.mask + 8ll * q, kWhole, kVec);
+    r.template write<kVec>(a, q, kWhole, set, k < split ? w_c : w_r);
   }
+  if (edge >= 0) own.template write<false>(a, edge, own.range(edge), edge_set, side_c ? w_c : w_r);
   if (b == 0 && a.t.cu != nullptr) {   // tokens outside every sequence
     const long long first = sequence_first(a.t, 0), last = sequence_first(a.t, a.t.S);
     for (long long i = member; i < first; i += team) a.grad[i] = 0.f;
@@ -644,39 +1059,35 @@ __device__ __forceinline__ float preference_pair(const PreferenceArgs& a, long l
   return loss;
 }
 
-// A cluster takes a pair; the last block to finish averages the pairs' losses.
-template <typename T>
-__global__ void __launch_bounds__(kPairThreads) preference_kernel(const PreferenceArgs a) {
-  struct Part {
-    Sum c, r;
-    long long n;
-  };
-  __shared__ Part s_part;
-  cg::cluster_group cluster = cg::this_cluster();
-  const int blocks = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+// A cluster takes a pair (kSeveral: it has more than one block); the last block to
+// finish averages the pairs' losses.
+template <typename T, bool kVec, bool kSeveral>
+__global__ void __launch_bounds__(kPairThreads, 3) preference_kernel(const PreferenceArgs a) {
+  int blocks = 1, rank = 0;
+  if (kSeveral) {
+    cg::cluster_group cluster = cg::this_cluster();
+    blocks = static_cast<int>(cluster.num_blocks());
+    rank = static_cast<int>(cluster.block_rank());
+  }
   const long long b = blockIdx.x / blocks;
-  const float loss = preference_pair<T>(
-      a, b, rank * kPairThreads + threadIdx.x, blocks * kPairThreads,
-      [&](Sum& c, Sum& r, long long& n) {
-        c = block_total(c);
-        r = block_total(r);
-        n = block_total(n);
-        if (blocks == 1) return;
-        if (threadIdx.x == 0) s_part = Part{c, r, n};
-        cluster.sync();
-        c = r = Sum{};
-        n = 0;
-        for (int i = 0; i < blocks; ++i) {
-          const Part* o = cluster.map_shared_rank(&s_part, i);
-          c = c + o->c;
-          r = r + o->r;
-          n += o->n;
-        }
-      });
-  if (blocks > 1) cluster.sync();   // s_part stays until it has been read
-  if (rank == 0 && threadIdx.x == 0 && store_allowed(a.pair_loss + b, 4, a.r_ws, a.status))
-    a.pair_loss[b] = loss;
-  if (!last_block(a.done)) return;
+  const int member = rank * kPairThreads + threadIdx.x, team = blocks * kPairThreads;
+  float loss;
+  if constexpr (kSeveral) {
+    loss = preference_pair<T, kVec>(a, b, member, team, ClusterTeam{});
+    cg::this_cluster().sync();   // a block's sums stay until the others have read them
+  } else {
+    loss = preference_pair<T, kVec>(a, b, member, team, BlockTeam{});
+  }
+  __shared__ bool s_last;
+  if (threadIdx.x == 0) {
+    s_last = false;
+    if (rank == 0) {
+      if (store_allowed(a.pair_loss + b, 4, a.r_ws, a.status)) a.pair_loss[b] = loss;
+      s_last = counted_last(a.done, static_cast<int>(a.t.S / 2));
+    }
+  }
+  __syncthreads();
+  if (!s_last) return;
   Sum sum{};
   for (long long i = threadIdx.x; i < a.t.S / 2; i += kPairThreads) sum.add(__ldcg(a.pair_loss + i));
   sum = block_total(sum);
@@ -684,19 +1095,17 @@ __global__ void __launch_bounds__(kPairThreads) preference_kernel(const Preferen
 }
 
 // One cluster; its blocks take the pairs in turn.
-template <typename T>
+template <typename T, bool kVec>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPairThreads)
     preference_small_kernel(const PreferenceArgs a) {
   __shared__ Sum s_loss;
   cg::cluster_group cluster = cg::this_cluster();
   const long long pairs = a.t.S / 2;
   Sum loss{};
-  for (long long b = blockIdx.x; b < pairs; b += kCluster)
-    loss.add(preference_pair<T>(a, b, threadIdx.x, kPairThreads, [](Sum& c, Sum& r, long long& n) {
-      c = block_total(c);
-      r = block_total(r);
-      n = block_total(n);
-    }));
+  for (long long b = blockIdx.x; b < pairs; b += kCluster) {
+    loss.add(preference_pair<T, kVec>(a, b, threadIdx.x, kPairThreads, BlockTeam{}));
+    __syncthreads();   // its shared memory is free for the next pair
+  }
   if (threadIdx.x == 0) s_loss = loss;
   cluster.sync();
   if (blockIdx.x == 0 && threadIdx.x == 0) {
@@ -756,23 +1165,29 @@ cudaError_t launch_policy(const PolicyArgs& a, int dtype, bool after_count, unsi
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = after_count ? 1 : 0;
-  const auto go = [&](auto* kernel) { return launch_with(attr, grid, kThreads, s, kernel, a); };
+  const auto pick = [&](auto* octets, auto* flat, auto* strided) {
+    return launch_with(attr, grid, kThreads, s, a.octets ? octets : a.flat ? flat : strided, a);
+  };
   if (dtype == FLCE_BF16)
-    return a.flat ? go(policy_kernel<__nv_bfloat16, true>) : go(policy_kernel<__nv_bfloat16, false>);
+    return pick(policy_octets_kernel<__nv_bfloat16>, policy_kernel<__nv_bfloat16, true>,
+                policy_kernel<__nv_bfloat16, false>);
   if (dtype == FLCE_F16)
-    return a.flat ? go(policy_kernel<__half, true>) : go(policy_kernel<__half, false>);
-  return a.flat ? go(policy_kernel<float, true>) : go(policy_kernel<float, false>);
+    return pick(policy_octets_kernel<__half>, policy_kernel<__half, true>, policy_kernel<__half, false>);
+  return pick(policy_octets_kernel<float>, policy_kernel<float, true>, policy_kernel<float, false>);
 }
 
 cudaError_t launch_preference_small(const PreferenceArgs& a, int dtype, cudaStream_t s) {
+  const auto go = [&](auto* kernel) {
+    kernel<<<kCluster, kPairThreads, 0, s>>>(a);
+    note_launch();
+    return cudaGetLastError();
+  };
   if (dtype == FLCE_BF16)
-    preference_small_kernel<__nv_bfloat16><<<kCluster, kPairThreads, 0, s>>>(a);
-  else if (dtype == FLCE_F16)
-    preference_small_kernel<__half><<<kCluster, kPairThreads, 0, s>>>(a);
-  else
-    preference_small_kernel<float><<<kCluster, kPairThreads, 0, s>>>(a);
-  note_launch();
-  return cudaGetLastError();
+    return a.vec ? go(preference_small_kernel<__nv_bfloat16, true>)
+                 : go(preference_small_kernel<__nv_bfloat16, false>);
+  if (dtype == FLCE_F16)
+    return a.vec ? go(preference_small_kernel<__half, true>) : go(preference_small_kernel<__half, false>);
+  return a.vec ? go(preference_small_kernel<float, true>) : go(preference_small_kernel<float, false>);
 }
 
 cudaError_t launch_preference(const PreferenceArgs& a, int dtype, int cluster, cudaStream_t s) {
@@ -781,10 +1196,17 @@ cudaError_t launch_preference(const PreferenceArgs& a, int dtype, int cluster, c
   attr.val.clusterDim.x = static_cast<unsigned>(cluster);
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
   const unsigned grid = static_cast<unsigned>(a.t.S / 2) * static_cast<unsigned>(cluster);
+  const auto pick = [&](auto* several, auto* one) {
+    return launch_with(attr, grid, kPairThreads, s, cluster > 1 ? several : one, a);
+  };
   if (dtype == FLCE_BF16)
-    return launch_with(attr, grid, kPairThreads, s, preference_kernel<__nv_bfloat16>, a);
-  if (dtype == FLCE_F16) return launch_with(attr, grid, kPairThreads, s, preference_kernel<__half>, a);
-  return launch_with(attr, grid, kPairThreads, s, preference_kernel<float>, a);
+    return a.vec ? pick(preference_kernel<__nv_bfloat16, true, true>, preference_kernel<__nv_bfloat16, true, false>)
+                 : pick(preference_kernel<__nv_bfloat16, false, true>, preference_kernel<__nv_bfloat16, false, false>);
+  if (dtype == FLCE_F16)
+    return a.vec ? pick(preference_kernel<__half, true, true>, preference_kernel<__half, true, false>)
+                 : pick(preference_kernel<__half, false, true>, preference_kernel<__half, false, false>);
+  return a.vec ? pick(preference_kernel<float, true, true>, preference_kernel<float, true, false>)
+               : pick(preference_kernel<float, false, true>, preference_kernel<float, false, false>);
 }
 
 }  // namespace flce

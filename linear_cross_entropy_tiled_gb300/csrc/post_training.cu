@@ -40,7 +40,7 @@ int check_tokens(const flce_tokens& t) {
     if (!aligned(t.cu_seqlens, 4)) return refuse(FLCE_ERR_ALIGNMENT, "cu_seqlens");
   } else {
     if (t.cols < 0 || t.cols > 2147483647ll - 1024 ||
-        (t.sequences > 0 && t.cols > (int64_t(1) << 40) / t.sequences))
+        (t.sequences > 0 && t.cols > (int64_t(1) << 39) / t.sequences))
       return refuse(FLCE_ERR_INVALID_ARG, "cols");
     if (t.cu_seqlens != nullptr) return refuse(FLCE_ERR_INVALID_ARG, "cu_seqlens without packed");
   }
@@ -115,9 +115,9 @@ bool contiguous(const flce_tokens& t, const void* p, int64_t ld) {
   return p == nullptr || t.packed || t.sequences <= 1 || ld == t.cols;
 }
 
-// Four neighbouring tokens, from a group's first one on, are aligned.
-bool groups_aligned(const flce_tokens& t, bool flat, const void* p, int64_t ld, size_t elem) {
-  return p == nullptr || (aligned(p, 4 * elem) && (flat || t.sequences <= 1 || ld % 4 == 0));
+// n neighbouring tokens, from a multiple of n on, are aligned to n elements.
+bool groups_aligned(const flce_tokens& t, bool flat, const void* p, int64_t ld, size_t elem, int n) {
+  return p == nullptr || (aligned(p, n * elem) && (flat || t.sequences <= 1 || ld % n == 0));
 }
 
 struct PolicyLayout {
@@ -268,18 +268,23 @@ int flce_policy_loss(const flce_policy_args* a, flce_stream_t stream) {
   k.ratio_lo = static_cast<float>(1.0 - a->clip_low);
   k.ratio_hi = static_cast<float>(1.0 + a->clip_high);
   k.dual = static_cast<float>(a->dual_clip);
-  k.log_dual = a->dual_clip > 0.0 ? static_cast<float>(log(a->dual_clip)) : 0.f;
+  k.log_dual = a->dual_clip > 0.0 ? static_cast<float>(log(a->dual_clip)) : INFINITY;
   k.kl_coef = static_cast<float>(a->kl_coef);
   k.adv_per_token = a->advantage_per_token;
   k.kl = a->kl_estimator;
   k.reduction = a->reduction;
   k.flat = L.flat ? 1 : 0;
-  k.vec = groups_aligned(t, L.flat, a->log_probs, a->ld_log_probs, elem) &&
-          groups_aligned(t, L.flat, a->old_log_probs, a->ld_old, elem) &&
-          (a->kl_coef == 0.0 || groups_aligned(t, L.flat, a->ref_log_probs, a->ld_ref, elem)) &&
-          (!a->advantage_per_token || groups_aligned(t, L.flat, a->advantages, a->ld_advantages, 4));
-  k.vec_mask = t.mask_kind == FLCE_MASK_BYTES && groups_aligned(t, L.flat, t.mask, t.ld_mask, 1);
-  k.vec_grad = groups_aligned(t, L.flat, a->grad, a->ld_grad, 4);
+  const auto inputs_aligned = [&](int n) {
+    return groups_aligned(t, L.flat, a->log_probs, a->ld_log_probs, elem, n) &&
+           groups_aligned(t, L.flat, a->old_log_probs, a->ld_old, elem, n) &&
+           (a->kl_coef == 0.0 || groups_aligned(t, L.flat, a->ref_log_probs, a->ld_ref, elem, n)) &&
+           (!a->advantage_per_token || groups_aligned(t, L.flat, a->advantages, a->ld_advantages, 4, n));
+  };
+  k.vec = inputs_aligned(4);
+  k.vec_mask = t.mask_kind == FLCE_MASK_BYTES && groups_aligned(t, L.flat, t.mask, t.ld_mask, 1, 4);
+  k.vec_grad = groups_aligned(t, L.flat, a->grad, a->ld_grad, 4, 4);
+  k.octets = L.flat && inputs_aligned(8) && groups_aligned(t, true, a->grad, 0, 4, 8) &&
+             (t.mask_kind != FLCE_MASK_BYTES || groups_aligned(t, true, t.mask, 0, 1, 8));
   k.groups = L.groups;
   k.row_groups = L.row_groups;
   k.loss = a->loss;
@@ -295,9 +300,10 @@ int flce_policy_loss(const flce_policy_args* a, flce_stream_t stream) {
     return v != FLCE_OK ? v : finish_call(k.status, st);
   }
   const int64_t most = std::min<int64_t>(kMaxBlocks, int64_t(sms) * kPolicyBlocksPerSm);
-  k.per = (L.groups + most - 1) / most;
+  const int64_t units = k.octets ? token_total(t) / 8 : L.groups;
+  k.per = (units + most - 1) / most;
   k.per = (k.per + 255) / 256 * 256;   // whole rounds of a block's threads
-  const unsigned grid = static_cast<unsigned>((L.groups + k.per - 1) / k.per);
+  const unsigned grid = static_cast<unsigned>((units + k.per - 1) / k.per);
   k.done = reinterpret_cast<int*>(ws);
   k.counts = reinterpret_cast<long long*>(ws + L.counts_at);
   k.num_counts = L.counts;
@@ -364,10 +370,10 @@ int flce_preference_loss(const flce_preference_args* a, flce_stream_t stream) {
   k.rejected = a->rejected_rewards;
   k.flat = contiguous(t, a->log_probs, a->ld_log_probs) && contiguous(t, a->ref_log_probs, a->ld_ref) &&
            contiguous(t, a->grad, a->ld_grad) && contiguous(t, t.mask, t.ld_mask);
-  k.vec = groups_aligned(t, k.flat, a->log_probs, a->ld_log_probs, elem) &&
-          groups_aligned(t, k.flat, a->ref_log_probs, a->ld_ref, elem);
-  k.vec_mask = t.mask_kind == FLCE_MASK_BYTES && groups_aligned(t, k.flat, t.mask, t.ld_mask, 1);
-  k.vec_grad = groups_aligned(t, k.flat, a->grad, a->ld_grad, 4);
+  k.vec = groups_aligned(t, k.flat, a->log_probs, a->ld_log_probs, elem, 8) &&
+          groups_aligned(t, k.flat, a->ref_log_probs, a->ld_ref, elem, 8) &&
+          groups_aligned(t, k.flat, a->grad, a->ld_grad, 4, 8) &&
+          (t.mask_kind != FLCE_MASK_BYTES || groups_aligned(t, k.flat, t.mask, t.ld_mask, 1, 8));
   k.r_grad = DevRegion{a->grad, span(t, a->ld_grad) * 4};
   k.r_ws = DevRegion{ws, L.total};
   if ((v = debug_status(&k.status, st)) != FLCE_OK) return v;

@@ -36,13 +36,16 @@ struct TokenView {
 
 // A block's share of the reduced outputs.
 struct __align__(16) PolicyPartial {
-  float loss, loss_err, kl, kl_err;   // sums and their rounding errors
+  float gain, gain_err, kl, kl_err;   // sums and their rounding errors; gain = -loss
   long long both;                     // clipped tokens, and in the low 32 bits tokens that count
 };
 
 constexpr int kPolicySmallGroups = 8192;      // groups of 4 tokens in one cluster of 8 x 1024 threads
 constexpr int kPolicySmallSequences = 1024;   // sequences whose tokens it can count ("sequence_mean")
-constexpr int kPolicyBlocksPerSm = 4;
+#ifndef PBS
+#define PBS 3
+#endif
+constexpr int kPolicyBlocksPerSm = PBS;
 
 struct PolicyArgs {
   TokenView t;
@@ -53,7 +56,7 @@ struct PolicyArgs {
   float* grad;                 // nullable
   long long ld_lp, ld_old, ld_ref, ld_adv, ld_grad;
   float sign;                  // -1: lp holds -log p
-  float lo, hi, ratio_lo, ratio_hi, log_dual, dual, kl_coef;   // dual: 0 off
+  float lo, hi, ratio_lo, ratio_hi, log_dual, dual, kl_coef;   // log_dual: +inf off
   int adv_per_token, kl, reduction;
   // Every token tensor is contiguous: a token has the same offset in all.
   // Else a token's offset is row * ld + column.
@@ -68,7 +71,8 @@ struct PolicyArgs {
   float* kl_sum;
   int* status;                 // nullable; written by FLCE_DEBUG builds
   // Large batches
-  long long per;               // groups a block of the streaming kernel
+  int octets;                  // flat, and eight neighbours are aligned in every tensor
+  long long per;               // groups (octets: of 8 tokens) a block of the streaming kernel
   int* done;                   // 0 before the streaming kernel
   long long* counts;           // tokens that count: num_counts parts, or one a sequence
   long long num_counts;        // 0: no mask
@@ -86,7 +90,8 @@ struct PreferenceArgs {
   float* grad;                 // nullable
   long long ld_lp, ld_ref, ld_grad;
   float sign;
-  int flat, vec, vec_mask, vec_grad;   // as PolicyArgs
+  int flat;                    // as PolicyArgs
+  int vec;                     // eight neighbours are aligned in every tensor (a label mask may not be)
   float beta, smoothing, margin;
   int type, average;
   float* loss;

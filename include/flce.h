@@ -544,7 +544,8 @@ typedef enum {
  * Token tensors need the alignment of their element only.
  * workspace: flce_policy_workspace_bytes, 16-byte aligned, any contents. Small
  * batches need none (0 bytes: workspace may be NULL), and no batch of at most
- * 8192 tokens and 1024 sequences needs one.
+ * 8192 tokens and 1024 sequences needs one; no batch needs more than 49152
+ * bytes and 8 for each sequence.
  */
 typedef struct {
   flce_tokens tokens;
@@ -590,7 +591,8 @@ int flce_policy_loss(const flce_policy_args* a, flce_stream_t stream);
  * and loss is the mean over pairs (NaN if there are none). chosen_rewards and
  * rejected_rewards hold beta s (nullable). ref may be NULL (no reference:
  * log_prob alone). The other conventions are flce_policy_loss's; no batch of at
- * most 8192 tokens and 64 pairs needs a workspace.
+ * most 8192 tokens and 64 pairs needs a workspace, and none needs more than
+ * 256 bytes and 4 for each pair.
  */
 typedef enum { FLCE_PREF_SIGMOID = 0, FLCE_PREF_HINGE = 1, FLCE_PREF_IPO = 2 } flce_preference;
 

@@ -32,10 +32,7 @@ namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;          // streaming and counting kernels
 constexpr int kSmallThreads = 1024;    // policy_small_kernel
-#ifndef PTH
-#define PTH 256
-#endif
-constexpr int kPairThreads = PTH;      // preference kernels
+constexpr int kPairThreads = 256;      // preference kernels (512: 41 us for 512 pairs of 2 x 8192 tokens, not 26)
 constexpr int kCluster = 8;
 
 // ------------------------------------------------------------- reductions
@@ -387,6 +384,21 @@ struct Totals {
   Sum gain, kl;
   long long clipped, tokens;
 };
+__device__ __forceinline__ Totals operator+(const Totals& a, const Totals& b) {
+  return Totals{a.gain + b.gain, a.kl + b.kl, a.clipped + b.clipped, a.tokens + b.tokens};
+}
+__device__ __forceinline__ Totals shuffle_xor(const Totals& v, int o) {
+  return Totals{shuffle_xor(v.gain, o), shuffle_xor(v.kl, o), shuffle_xor(v.clipped, o),
+                shuffle_xor(v.tokens, o)};
+}
+// The same of a block's share, whose counts fit 32 bits.
+__device__ __forceinline__ Running operator+(const Running& a, const Running& b) {
+  return Running{a.gain + b.gain, a.kl + b.kl, a.clipped + b.clipped, a.tokens + b.tokens};
+}
+__device__ __forceinline__ Running shuffle_xor(const Running& v, int o) {
+  return Running{shuffle_xor(v.gain, o), shuffle_xor(v.kl, o), shuffle_xor(v.clipped, o),
+                 shuffle_xor(v.tokens, o)};
+}
 
 __device__ __forceinline__ void policy_outputs(const PolicyArgs& a, const Totals& v) {
   const bool none = (a.reduction == FLCE_TOKEN_MEAN && v.tokens == 0) ||
@@ -464,9 +476,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads
   if (g.bits != 0) policy_group(a, g.bits, x, old, ref, adv, weight, out, v);
   if (a.grad != nullptr && q < a.groups)
     store4(a.grad + g.index(a.ld_grad), g.range, a.vec_grad && g.whole, out, a.r_grad, a.status);
-  v.gain = block_total(v.gain);
-  v.kl = block_total(v.kl);
-  v.clipped = block_total(v.clipped);
+  v = block_total(v);
   if (threadIdx.x == 0) {
     s_totals.gain = v.gain;
     s_totals.kl = v.kl;
@@ -594,14 +604,11 @@ struct Sequence {
 
 // A block's share of the outputs; the last block to finish adds them up.
 __device__ __forceinline__ void policy_finish(const PolicyArgs& a, Running& v) {
-  v.gain = block_total(v.gain);
-  v.kl = block_total(v.kl);
-  const long long both = block_total(static_cast<long long>(v.clipped) << 32 |
-                                     static_cast<long long>(v.tokens));
+  v = block_total(v);
   __shared__ bool s_last;
   if (threadIdx.x == 0) {
     if (store_allowed(a.partials + blockIdx.x, sizeof(PolicyPartial), a.r_ws, a.status))
-      a.partials[blockIdx.x] = PolicyPartial{v.gain.s, v.gain.c, v.kl.s, v.kl.c, both};
+      a.partials[blockIdx.x] = PolicyPartial{v.gain.s, v.gain.c, v.kl.s, v.kl.c, v.clipped, v.tokens};
     s_last = counted_last(a.done, static_cast<int>(gridDim.x));
   }
   __syncthreads();
@@ -610,16 +617,10 @@ __device__ __forceinline__ void policy_finish(const PolicyArgs& a, Running& v) {
   for (unsigned b = threadIdx.x; b < gridDim.x; b += kThreads) {
     const PolicyPartial* o = a.partials + b;
     const float4 f = __ldcg(reinterpret_cast<const float4*>(o));
-    const long long n = __ldcg(&o->both);
-    all.gain = all.gain + Sum{f.x, f.y};
-    all.kl = all.kl + Sum{f.z, f.w};
-    all.clipped += n >> 32;
-    all.tokens += n & 0xffffffffll;
+    const int2 n = __ldcg(reinterpret_cast<const int2*>(&o->clipped));
+    all = all + Totals{Sum{f.x, f.y}, Sum{f.z, f.w}, n.x, static_cast<unsigned>(n.y)};
   }
-  all.gain = block_total(all.gain);
-  all.kl = block_total(all.kl);
-  all.clipped = block_total(all.clipped);
-  all.tokens = block_total(all.tokens);
+  all = block_total(all);
   if (threadIdx.x == 0) policy_outputs(a, all);
 }
 
@@ -719,110 +720,136 @@ __device__ __forceinline__ void store_octet(float* p, unsigned range, const floa
     if (has(range, k) && store_allowed(p + k, 4, r, status)) p[k] = x[k];
 }
 
-// One octet of the contiguous streaming kernel: `set` of it counts, `range`
-// exists, p* point at it. `at` is its flat token.
-template <typename T, bool kVec>
-__device__ __forceinline__ void policy_octet(const PolicyArgs& a, long long at, unsigned set, unsigned range,
-                                             Sequence& seq, Running& v) {
-  float out[8] = {};
-  if (set != 0) {
-    float x[8], old[8], ref[8] = {}, adv[8], gain[8], slope[8], sum = 0.f;
+// One octet of the contiguous streaming kernel. `at` is its first token; `set`
+// of it counts. kRow: its tokens' sequences matter (an advantage or a weight
+// for each).
+template <typename T, bool kRow>
+struct Octet {
+  long long at;
+  unsigned set;
+  float x[8], old[8], ref[8], adv[8];
+
+  template <bool kVec>
+  __device__ __forceinline__ void read(const PolicyArgs& a) {
+    if (set == 0) return;
     load_octet<kVec>(static_cast<const T*>(a.lp) + at, set, x);
     if (a.old != nullptr) load_octet<kVec>(static_cast<const T*>(a.old) + at, set, old);
     if (a.kl_coef != 0.f) load_octet<kVec>(static_cast<const T*>(a.ref) + at, set, ref);
-    if (a.adv_per_token) load_octet<kVec>(a.adv + at, set, adv);
-    if (a.old == nullptr) {   // the log ratio is 0
+    if (!kRow || a.adv_per_token) load_octet<kVec>(a.adv + at, set, adv);
+  }
+
+  // Adds its terms to `v` and writes the gradient of `range`, what exists of it.
+  template <bool kVec>
+  __device__ __forceinline__ void step(const PolicyArgs& a, unsigned range, Sequence& seq, Running& v) {
+    float out[8] = {};
+    if (set != 0) {
+      float gain[8], slope[8], sum = 0.f;
+      if (a.old == nullptr) {   // the log ratio is 0
 #pragma unroll
-      for (int k = 0; k < 8; ++k) old[k] = a.sign * x[k];
-    }
-    const bool need_row = a.reduction == FLCE_SEQUENCE_MEAN || !a.adv_per_token;
-    const bool several = need_row && at + 7 >= seq.w.end;   // perhaps several sequences
-    Sequence again = seq;
-    if (!a.adv_per_token) {
+        for (int k = 0; k < 8; ++k) old[k] = a.sign * x[k];
+      }
+      const bool several = kRow && at + 7 >= seq.w.end;   // perhaps several sequences
+      Sequence again = seq;
+      if (kRow && !a.adv_per_token) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) adv[k] = seq.adv;
-      if (several) {
+        for (int k = 0; k < 8; ++k) adv[k] = seq.adv;
+        if (several) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (!has(set, k)) continue;
+            seq.w.to(a.t, at + k);
+            seq.enter(a);
+            adv[k] = seq.adv;
+          }
+        }
+      }
+      if (set != kWhole) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) silence(has(set, k), x[k], old[k], ref[k], adv[k]);
+      }
+      policy_tokens(a, x, old, ref, adv, gain, slope, v);
+      v.tokens += __popc(set);
+      if (kRow && several && a.reduction == FLCE_SEQUENCE_MEAN) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (!has(set, k)) continue;
-          seq.w.to(a.t, at + k);
-          seq.enter(a);
-          adv[k] = seq.adv;
+          again.w.to(a.t, at + k);
+          again.enter(a);
+          sum = fmaf(gain[k], again.weight, sum);
+          out[k] = slope[k] * (-a.sign * again.weight);
+        }
+        seq = again;
+      } else {
+        const float w = -a.sign * seq.weight;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          sum += gain[k];
+          out[k] = slope[k] * w;
+        }
+        sum *= seq.weight;
+        if (set != kWhole) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) out[k] = has(set, k) ? out[k] : 0.f;
         }
       }
+      v.gain.add(sum);
     }
-    if (set != kWhole) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) silence(has(set, k), x[k], old[k], ref[k], adv[k]);
-    }
-    policy_tokens(a, x, old, ref, adv, gain, slope, v);
-    v.tokens += __popc(set);
-    if (several && a.reduction == FLCE_SEQUENCE_MEAN) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        if (!has(set, k)) continue;
-        again.w.to(a.t, at + k);
-        again.enter(a);
-        sum = fmaf(gain[k], again.weight, sum);
-        out[k] = slope[k] * (-a.sign * again.weight);
-      }
-      seq = again;
-    } else {
-      const float w = -a.sign * seq.weight;
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        sum += gain[k];
-        out[k] = slope[k] * w;
-      }
-      sum *= seq.weight;
-      if (set != kWhole) {
-#pragma unroll
-        for (int k = 0; k < 8; ++k) out[k] = has(set, k) ? out[k] : 0.f;
-      }
-    }
-    v.gain.add(sum);
+    if (a.grad != nullptr) store_octet<kVec>(a.grad + at, range, out, a.r_grad, a.status);
   }
-  if (a.grad != nullptr) store_octet<kVec>(a.grad + at, range, out, a.r_grad, a.status);
-}
+};
 
 // The streaming kernel of contiguous, aligned batches: a.per octets a block,
 // kThreads at a time, the masks of the next ones on their way; the last few
 // tokens are the last block's.
-template <typename T>
+template <typename T, bool kRow>
 __global__ void __launch_bounds__(kThreads, kPolicyBlocksPerSm) policy_octets_kernel(const PolicyArgs a) {
   const long long octets = a.t.N / 8, o0 = blockIdx.x * a.per;
   const int count = static_cast<int>(min(octets - o0, a.per));
   const bool masked = a.t.mask_kind != FLCE_MASK_NONE;
-  int i = threadIdx.x;
-  unsigned next = kWhole;
-  if (masked && i < count) next = mask8(a.t, (o0 + i) * 8, kWhole, true);
   // the tokens that lie in sequences
   long long first = 0, end = a.t.N;
   if (a.t.cu != nullptr) {
     first = clamp_to(__ldg(a.t.cu), a.t.N);
     end = a.t.S > 0 ? clamp_to(__ldg(a.t.cu + a.t.S), a.t.N) : 0;
   }
+  const auto in_sequences = [&](long long at) {
+    return tokens_from_to(static_cast<int>(min(max(first - at, 0ll), 8ll)),
+                          static_cast<int>(min(max(end - at, 0ll), 8ll)));
+  };
   const bool inside = first <= o0 * 8 && (o0 + count) * 8 <= end;   // all of the block's
-  wait_for_previous();
+  int i = threadIdx.x;
+  unsigned next = kWhole;   // what counts of octet i + kThreads, then of those after it
+  Octet<T, kRow> o;
+  // the octet i, whose tokens that count are `set`
+  const auto read = [&](unsigned set) {
+    o.at = (o0 + i) * 8;
+    o.set = inside ? set : set & in_sequences(o.at);
+    o.template read<true>(a);
+  };
+  if (i < count) {
+    unsigned set = kWhole;
+    if (masked) set = mask8(a.t, (o0 + i) * 8, kWhole, true);
+    if (masked && i + kThreads < count) next = mask8(a.t, (o0 + i + kThreads) * 8, kWhole, true);
+    read(set);
+  }
+  wait_for_previous();   // up to here only the caller's tensors were read
   Sequence seq(batch_weight(a));
   Running v{};
-  for (; i < count; i += kThreads) {
-    unsigned set = next;
+  while (i < count) {
+    o.template step<true>(a, kWhole, seq, v);
+    i += kThreads;
+    if (i >= count) break;
+    const unsigned set = next;
     if (masked && i + kThreads < count) next = mask8(a.t, (o0 + i + kThreads) * 8, kWhole, true);
-    const long long at = (o0 + i) * 8;
-    if (!inside)
-      set &= tokens_from_to(static_cast<int>(min(max(first - at, 0ll), 8ll)),
-                            static_cast<int>(min(max(end - at, 0ll), 8ll)));
-    policy_octet<T, true>(a, at, set, kWhole, seq, v);
+    read(set);
   }
   const int tail = static_cast<int>(a.t.N - octets * 8);
   if (tail != 0 && blockIdx.x == gridDim.x - 1 && threadIdx.x == kThreads - 1) {
-    const long long at = octets * 8;
+    o.at = octets * 8;
     const unsigned range = tokens_from_to(0, tail);
-    const unsigned set = mask8(a.t, at, range, false) &
-                         tokens_from_to(static_cast<int>(min(max(first - at, 0ll), 8ll)),
-                                        static_cast<int>(min(max(end - at, 0ll), 8ll)));
-    policy_octet<T, false>(a, at, set, range, seq, v);
+    o.set = mask8(a.t, o.at, range, false) & in_sequences(o.at);
+    o.template read<false>(a);
+    o.template step<false>(a, range, seq, v);
   }
   policy_finish(a, v);
 }
@@ -886,8 +913,8 @@ struct Row {
   }
 };
 
-constexpr int kKept = 8;    // octets of a thread whose tokens that count stay in a register
-constexpr int kBatch = 2;   // octets that a thread reads at once
+constexpr int kKept = 8;    // octets of a thread whose masks are read at once, and the first ones kept
+constexpr int kBatch = 2;   // octets of a thread whose tokens are read at once
 
 // The sums and token counts of a pair's two sequences, of a warp, a block or
 // the whole team.
@@ -942,32 +969,44 @@ __device__ __forceinline__ float preference_pair(const PreferenceArgs& a, long l
   const int split = chosen.to - chosen.from, whole = split + rejected.to - rejected.from;
   const auto row_of = [&](int k) { return k < split ? chosen : rejected; };
   const auto octet_of = [&](int k) { return k < split ? k + chosen.from : k - split + rejected.from; };
+  // The tokens that count of a member's next kKept octets, from octet k on,
+  // eight bits each: so many loads on their way at once.
+  const auto sets_from = [&](int k) {
+    unsigned long long sets = ~0ull;
+    if (masked) {
+      sets = 0;
+#pragma unroll
+      for (int i = 0; i < kKept; ++i, k += team)
+        if (k < whole)
+          sets |= static_cast<unsigned long long>(
+                      mask8(a.t, row_of(k).mask + 8ll * octet_of(k), kWhole, kVec)) << (8 * i);
+    }
+    return sets;
+  };
   unsigned long long kept = 0;
-  int index = 0, n_c = 0, n_r = 0;
+  int n_c = 0, n_r = 0;
   Sum sum_c{}, sum_r{};
-  for (int j = member; j < whole; j += kBatch * team, index += kBatch) {
-    unsigned set[kBatch];
-    float d[kBatch];
+  for (int j = member; j < whole; j += kKept * team) {
+    unsigned long long sets = sets_from(j);
+    if (j == member) kept = sets;
+    for (int k = j; k < min(whole, j + kKept * team); k += kBatch * team, sets >>= 8 * kBatch) {
+      unsigned set[kBatch];
+      float d[kBatch];
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int k = j + i * team;
-      set[i] = k >= whole ? 0u
-               : masked ? mask8(a.t, row_of(k).mask + 8ll * octet_of(k), kWhole, kVec) : kWhole;
-      if (index + i < kKept) kept |= static_cast<unsigned long long>(set[i]) << (8 * (index + i));
-    }
+      for (int i = 0; i < kBatch; ++i) {
+        const int q = k + i * team;
+        set[i] = q < whole ? static_cast<unsigned>(sets >> (8 * i)) & kWhole : 0u;
+        d[i] = set[i] != 0 ? row_of(q).template sum<kVec>(a, octet_of(q), set[i]) : 0.f;
+      }
 #pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int k = j + i * team;
-      d[i] = set[i] != 0 ? row_of(k).template sum<kVec>(a, octet_of(k), set[i]) : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const bool first = j + i * team < split;
-      const int count = __popc(set[i]);
-      sum_c.add(first ? d[i] : 0.f);
-      sum_r.add(first ? 0.f : d[i]);
-      n_c += first ? count : 0;
-      n_r += first ? 0 : count;
+      for (int i = 0; i < kBatch; ++i) {
+        const bool first = k + i * team < split;
+        const int count = __popc(set[i]);
+        sum_c.add(first ? d[i] : 0.f);
+        sum_r.add(first ? 0.f : d[i]);
+        n_c += first ? count : 0;
+        n_r += first ? 0 : count;
+      }
     }
   }
   // Octets that are not whole: the first and the last of either sequence, the
@@ -1040,15 +1079,11 @@ __device__ __forceinline__ float preference_pair(const PreferenceArgs& a, long l
   __syncthreads();
   const float w_c = s_out[0], w_r = s_out[1], loss = s_out[2];
   if (a.grad == nullptr) return loss;
-  index = 0;
-  for (int k = member; k < whole; k += team, ++index) {
-    const Row<T> r = row_of(k);
-    const int q = octet_of(k);
-    unsigned set = kWhole;
-    if (masked)
-      set = index < kKept ? static_cast<unsigned>(kept >> (8 * index)) & kWhole
-                          : mask8(a.t, r.mask + 8ll * q, kWhole, kVec);
-    r.template write<kVec>(a, q, kWhole, set, k < split ? w_c : w_r);
+  for (int j = member; j < whole; j += kKept * team) {
+    unsigned long long sets = j == member ? kept : sets_from(j);
+    for (int k = j; k < min(whole, j + kKept * team); k += team, sets >>= 8)
+      row_of(k).template write<kVec>(a, octet_of(k), kWhole, static_cast<unsigned>(sets) & kWhole,
+                                     k < split ? w_c : w_r);
   }
   if (edge >= 0) own.template write<false>(a, edge, own.range(edge), edge_set, side_c ? w_c : w_r);
   if (b == 0 && a.t.cu != nullptr) {   // tokens outside every sequence
@@ -1062,7 +1097,7 @@ __device__ __forceinline__ float preference_pair(const PreferenceArgs& a, long l
 // A cluster takes a pair (kSeveral: it has more than one block); the last block to
 // finish averages the pairs' losses.
 template <typename T, bool kVec, bool kSeveral>
-__global__ void __launch_bounds__(kPairThreads, 3) preference_kernel(const PreferenceArgs a) {
+__global__ void __launch_bounds__(kPairThreads, 4) preference_kernel(const PreferenceArgs a) {
   int blocks = 1, rank = 0;
   if (kSeveral) {
     cg::cluster_group cluster = cg::this_cluster();
@@ -1165,15 +1200,19 @@ cudaError_t launch_policy(const PolicyArgs& a, int dtype, bool after_count, unsi
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = after_count ? 1 : 0;
-  const auto pick = [&](auto* octets, auto* flat, auto* strided) {
-    return launch_with(attr, grid, kThreads, s, a.octets ? octets : a.flat ? flat : strided, a);
+  const bool row = a.reduction == FLCE_SEQUENCE_MEAN || !a.adv_per_token;
+  const auto pick = [&](auto* tokens, auto* rows, auto* flat, auto* strided) {
+    return launch_with(attr, grid, kThreads, s,
+                       a.octets ? (row ? rows : tokens) : a.flat ? flat : strided, a);
   };
   if (dtype == FLCE_BF16)
-    return pick(policy_octets_kernel<__nv_bfloat16>, policy_kernel<__nv_bfloat16, true>,
-                policy_kernel<__nv_bfloat16, false>);
+    return pick(policy_octets_kernel<__nv_bfloat16, false>, policy_octets_kernel<__nv_bfloat16, true>,
+                policy_kernel<__nv_bfloat16, true>, policy_kernel<__nv_bfloat16, false>);
   if (dtype == FLCE_F16)
-    return pick(policy_octets_kernel<__half>, policy_kernel<__half, true>, policy_kernel<__half, false>);
-  return pick(policy_octets_kernel<float>, policy_kernel<float, true>, policy_kernel<float, false>);
+    return pick(policy_octets_kernel<__half, false>, policy_octets_kernel<__half, true>,
+                policy_kernel<__half, true>, policy_kernel<__half, false>);
+  return pick(policy_octets_kernel<float, false>, policy_octets_kernel<float, true>,
+              policy_kernel<float, true>, policy_kernel<float, false>);
 }
 
 cudaError_t launch_preference_small(const PreferenceArgs& a, int dtype, cudaStream_t s) {

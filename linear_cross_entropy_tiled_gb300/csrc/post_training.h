@@ -37,15 +37,12 @@ struct TokenView {
 // A block's share of the reduced outputs.
 struct __align__(16) PolicyPartial {
   float gain, gain_err, kl, kl_err;   // sums and their rounding errors; gain = -loss
-  long long both;                     // clipped tokens, and in the low 32 bits tokens that count
+  int clipped, tokens;                // tokens: unsigned
 };
 
 constexpr int kPolicySmallGroups = 8192;      // groups of 4 tokens in one cluster of 8 x 1024 threads
 constexpr int kPolicySmallSequences = 1024;   // sequences whose tokens it can count ("sequence_mean")
-#ifndef PBS
-#define PBS 3
-#endif
-constexpr int kPolicyBlocksPerSm = PBS;
+constexpr int kPolicyBlocksPerSm = 3;   // of the streaming kernels (80 registers; 2 and 4 are slower)
 
 struct PolicyArgs {
   TokenView t;

@@ -23,7 +23,10 @@ from . import _lib
 from .functional import (_DTYPES, _maybe_check, _params, _prepare, _ptr, _stream, flce_backward,
                          flce_forward)
 
-_SMALL = 8192   # tokens; batches of no more need no workspace (include/flce.h)
+# Workspace bounds of include/flce.h: none for this many tokens, else so many
+# bytes and 8 (preference loss: 4) for each sequence (pair).
+_SMALL = 8192
+_POLICY_WORKSPACE, _PREFERENCE_WORKSPACE = 49152, 256
 
 
 def _laid_out(t: torch.Tensor, shape, dtype, device, name: str):
@@ -102,7 +105,7 @@ def _policy(tokens, sequences, log_probs, old, advantages, ref, clip_low, clip_h
         advantages, ld_adv = _laid_out(advantages, shape, torch.float32, dev, "advantages")
         per_token = 1
     elif a_shape == (sequences,) or a_shape == (sequences, 1):
-        advantages = advantages.reshape(sequences).contiguous()
+        advantages = advantages.contiguous()
     else:
         raise ValueError(f"advantages must be [{sequences}], one per sequence, or {tuple(shape)}, "
                          f"one per token; got {tuple(a_shape)}")
@@ -116,28 +119,29 @@ def _policy(tokens, sequences, log_probs, old, advantages, ref, clip_low, clip_h
     elif kl_coef:
         raise ValueError("kl_coef needs ref_log_probs")
     grad = torch.empty(shape, dtype=torch.float32, device=dev)
-    out = torch.empty(2, dtype=torch.float32, device=dev)
-    loss_at = out.data_ptr()
-    kl_at = n_at = clipped_at = 0
+    n = grad.numel()
+    ws_at = ws_bytes = n_at = clipped_at = kl_at = 0
+    if n > _SMALL or sequences > 1024:
+        ws = torch.empty(_POLICY_WORKSPACE + 8 * sequences, dtype=torch.uint8, device=dev)
+        ws_at, ws_bytes = ws.data_ptr(), ws.numel()
     if return_metrics:
-        n = torch.empty(2, dtype=torch.int64, device=dev)
-        kl_at, n_at = loss_at + 4, n.data_ptr()
-        clipped_at = n_at + 8
-
-    def pack(ws, ws_bytes):
-        return _lib.POLICY_ARGS.pack(
-            *tokens, log_probs.data_ptr(), old_at, ref_at, advantages.data_ptr(), loss_at,
-            grad.data_ptr(), n_at, clipped_at, kl_at, ws, ws_bytes, ld, ld_old, ld_ref, ld_adv,
-            shape[-1], clip_low, clip_high, dual_clip or 0.0, kl_coef, _DTYPES[dtype], per_token,
-            estimator, reduce, negated, 0)
-    args = pack(0, 0)
-    if grad.numel() > _SMALL or sequences > 1024:
-        ws = torch.empty(max(16, _lib.policy_workspace_bytes(args)), dtype=torch.uint8, device=dev)
-        args = pack(ws.data_ptr(), ws.numel())
+        # loss and KL sum as two floats, then the two counts
+        counts = torch.empty(3, dtype=torch.int64, device=dev)
+        out = counts.view(torch.float32)
+        loss_at = counts.data_ptr()
+        kl_at, n_at, clipped_at = loss_at + 4, loss_at + 8, loss_at + 16
+    else:
+        out = torch.empty(1, dtype=torch.float32, device=dev)
+        loss_at = out.data_ptr()
+    args = _lib.POLICY_ARGS.pack(
+        *tokens, log_probs.data_ptr(), old_at, ref_at, advantages.data_ptr(), loss_at,
+        grad.data_ptr(), n_at, clipped_at, kl_at, ws_at, ws_bytes, ld, ld_old, ld_ref, ld_adv,
+        shape[-1], clip_low, clip_high, dual_clip or 0.0, kl_coef, _DTYPES[dtype], per_token,
+        estimator, reduce, negated, 0)
     _lib.check(_lib.policy_loss_raw(args, _stream(dev)), "flce_policy_loss")
     if not return_metrics:
         return out[0], grad, None
-    return out[0], grad, {"num_tokens": n[0], "num_clipped": n[1], "kl_sum": out[1]}
+    return out[0], grad, {"num_tokens": counts[1], "num_clipped": counts[2], "kl_sum": out[1]}
 
 
 def policy_loss_and_grad(log_probs: torch.Tensor, old_log_probs: Optional[torch.Tensor],
@@ -187,15 +191,14 @@ def _preference(tokens, sequences, log_probs, ref, beta, loss_type, label_smooth
     out = torch.empty(1 + 2 * pairs, dtype=torch.float32, device=dev)
     at = out.data_ptr()
 
-    def pack(ws, ws_bytes):
-        return _lib.PREFERENCE_ARGS.pack(
-            *tokens, log_probs.data_ptr(), ref_at, at, grad.data_ptr(), at + 4, at + 4 + 4 * pairs,
-            ws, ws_bytes, ld, ld_ref, shape[-1], beta, label_smoothing, margin, _DTYPES[dtype], kind,
-            1 if average else 0, negated)
-    args = pack(0, 0)
+    ws_at = ws_bytes = 0
     if grad.numel() > _SMALL or pairs > 64:
-        ws = torch.empty(max(16, _lib.preference_workspace_bytes(args)), dtype=torch.uint8, device=dev)
-        args = pack(ws.data_ptr(), ws.numel())
+        ws = torch.empty(_PREFERENCE_WORKSPACE + 4 * pairs, dtype=torch.uint8, device=dev)
+        ws_at, ws_bytes = ws.data_ptr(), ws.numel()
+    args = _lib.PREFERENCE_ARGS.pack(
+        *tokens, log_probs.data_ptr(), ref_at, at, grad.data_ptr(), at + 4, at + 4 + 4 * pairs,
+        ws_at, ws_bytes, ld, ld_ref, shape[-1], beta, label_smoothing, margin, _DTYPES[dtype], kind,
+        1 if average else 0, negated)
     _lib.check(_lib.preference_loss_raw(args, _stream(dev)), "flce_preference_loss")
     return out[0], grad, out[1:1 + pairs], out[1 + pairs:]
 

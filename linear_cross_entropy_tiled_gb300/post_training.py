@@ -85,6 +85,25 @@ def _label_tokens(nll, labels, ignore_index, cu_seqlens):
             _lib.FLCE_MASK_LABELS), n, keep
 
 
+def _float_like(x: torch.Tensor, shape, device) -> torch.Tensor:
+    """A new contiguous float32 tensor of the log probabilities' shape."""
+    if x.dtype is torch.float32 and x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(shape, dtype=torch.float32, device=device)
+
+
+_templates: dict = {}
+
+
+def _scalar_templates(device):
+    """A float32 and an int64 scalar of the device for empty_like, the quickest way to new scalars."""
+    t = _templates.get(device)
+    if t is None:
+        t = _templates[device] = (torch.empty((), dtype=torch.float32, device=device),
+                                  torch.empty((), dtype=torch.int64, device=device))
+    return t
+
+
 def _option(table: dict, value: str, name: str) -> int:
     if value not in table:
         raise ValueError(f"{name} must be one of {tuple(table)}, got {value!r}")
@@ -118,30 +137,24 @@ def _policy(tokens, sequences, log_probs, old, advantages, ref, clip_low, clip_h
         ref_at = ref.data_ptr()
     elif kl_coef:
         raise ValueError("kl_coef needs ref_log_probs")
-    grad = torch.empty(shape, dtype=torch.float32, device=dev)
-    n = grad.numel()
-    ws_at = ws_bytes = n_at = clipped_at = kl_at = 0
-    if n > _SMALL or sequences > 1024:
+    grad = _float_like(log_probs, shape, dev)
+    ws_at = ws_bytes = 0
+    if grad.numel() > _SMALL or sequences > 1024:
         ws = torch.empty(_POLICY_WORKSPACE + 8 * sequences, dtype=torch.uint8, device=dev)
         ws_at, ws_bytes = ws.data_ptr(), ws.numel()
+    f0, i0 = _scalar_templates(dev)
+    loss, metrics, kl_at, n_at, clipped_at = torch.empty_like(f0), None, 0, 0, 0
     if return_metrics:
-        # loss and KL sum as two floats, then the two counts
-        counts = torch.empty(3, dtype=torch.int64, device=dev)
-        out = counts.view(torch.float32)
-        loss_at = counts.data_ptr()
-        kl_at, n_at, clipped_at = loss_at + 4, loss_at + 8, loss_at + 16
-    else:
-        out = torch.empty(1, dtype=torch.float32, device=dev)
-        loss_at = out.data_ptr()
+        kl_sum, n, clipped = torch.empty_like(f0), torch.empty_like(i0), torch.empty_like(i0)
+        kl_at, n_at, clipped_at = kl_sum.data_ptr(), n.data_ptr(), clipped.data_ptr()
+        metrics = {"num_tokens": n, "num_clipped": clipped, "kl_sum": kl_sum}
     args = _lib.POLICY_ARGS.pack(
-        *tokens, log_probs.data_ptr(), old_at, ref_at, advantages.data_ptr(), loss_at,
+        *tokens, log_probs.data_ptr(), old_at, ref_at, advantages.data_ptr(), loss.data_ptr(),
         grad.data_ptr(), n_at, clipped_at, kl_at, ws_at, ws_bytes, ld, ld_old, ld_ref, ld_adv,
         shape[-1], clip_low, clip_high, dual_clip or 0.0, kl_coef, _DTYPES[dtype], per_token,
         estimator, reduce, negated, 0)
     _lib.check(_lib.policy_loss_raw(args, _stream(dev)), "flce_policy_loss")
-    if not return_metrics:
-        return out[0], grad, None
-    return out[0], grad, {"num_tokens": counts[1], "num_clipped": counts[2], "kl_sum": out[1]}
+    return loss, grad, metrics
 
 
 def policy_loss_and_grad(log_probs: torch.Tensor, old_log_probs: Optional[torch.Tensor],
@@ -187,20 +200,21 @@ def _preference(tokens, sequences, log_probs, ref, beta, loss_type, label_smooth
         ref, ld_ref = _laid_out(ref, shape, dtype, dev, "ref_log_probs")
         ref_at = ref.data_ptr()
     pairs = sequences // 2
-    grad = torch.empty(shape, dtype=torch.float32, device=dev)
-    out = torch.empty(1 + 2 * pairs, dtype=torch.float32, device=dev)
-    at = out.data_ptr()
+    grad = _float_like(log_probs, shape, dev)
+    loss = torch.empty_like(_scalar_templates(dev)[0])
+    chosen = torch.empty(pairs, dtype=torch.float32, device=dev)
+    rejected = torch.empty_like(chosen)
 
     ws_at = ws_bytes = 0
     if grad.numel() > _SMALL or pairs > 64:
         ws = torch.empty(_PREFERENCE_WORKSPACE + 4 * pairs, dtype=torch.uint8, device=dev)
         ws_at, ws_bytes = ws.data_ptr(), ws.numel()
     args = _lib.PREFERENCE_ARGS.pack(
-        *tokens, log_probs.data_ptr(), ref_at, at, grad.data_ptr(), at + 4, at + 4 + 4 * pairs,
-        ws_at, ws_bytes, ld, ld_ref, shape[-1], beta, label_smoothing, margin, _DTYPES[dtype], kind,
+        *tokens, log_probs.data_ptr(), ref_at, loss.data_ptr(), grad.data_ptr(), chosen.data_ptr(),
+        rejected.data_ptr(), ws_at, ws_bytes, ld, ld_ref, shape[-1], beta, label_smoothing, margin, _DTYPES[dtype], kind,
         1 if average else 0, negated)
     _lib.check(_lib.preference_loss_raw(args, _stream(dev)), "flce_preference_loss")
-    return out[0], grad, out[1:1 + pairs], out[1 + pairs:]
+    return loss, grad, chosen, rejected
 
 
 def preference_loss_and_grad(log_probs: torch.Tensor, ref_log_probs: Optional[torch.Tensor] = None,

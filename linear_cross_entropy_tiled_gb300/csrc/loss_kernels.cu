@@ -180,22 +180,24 @@ __device__ __forceinline__ long long sequence_end(const TokenView& t, long long 
 // The sequence that flat token i lies in, and its end, walking on from an
 // earlier one.
 struct Walker {
-  long long s = 0, end = -1;
+  int s = 0;
+  long long end = -1;
   __device__ __forceinline__ void to(const TokenView& t, long long i) {
     if (i < end) return;
     if (t.cu == nullptr) {
-      s = t.N <= 0x7fffffffll ? static_cast<unsigned>(i) / static_cast<unsigned>(t.cols) : i / t.cols;
-      end = (s + 1) * t.cols;
+      s = t.N <= 0x7fffffffll ? static_cast<unsigned>(i) / static_cast<unsigned>(t.cols)
+                              : static_cast<int>(i / t.cols);
+      end = (s + 1ll) * t.cols;
       return;
     }
     // the last sequence that begins at or before i: doubling steps, then halving ones
-    long long step = 1;
-    while (s + step < t.S && __ldg(t.cu + s + step) <= i) {
+    int step = 1;
+    while (step < t.S - s && __ldg(t.cu + s + step) <= i) {
       s += step;
       step *= 2;
     }
     for (; step >= 1; step /= 2)
-      if (s + step < t.S && __ldg(t.cu + s + step) <= i) s += step;
+      if (step < t.S - s && __ldg(t.cu + s + step) <= i) s += step;
     end = sequence_end(t, s, 0);
   }
 };
@@ -440,8 +442,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       if (!(g.bits >> k & 1u)) continue;
-      if (kFlat) w.to(a.t, g.at + k); else w.s = g.row;
-      row[k] = static_cast<int>(w.s);
+      if (kFlat) w.to(a.t, g.at + k); else w.s = static_cast<int>(g.row);
+      row[k] = w.s;
       if (count_rows) atomicAdd(s_count + row[k], 1);
       if (!a.adv_per_token) adv[k] = __ldg(a.adv + row[k]);
     }
@@ -538,45 +540,15 @@ __global__ void __launch_bounds__(kThreads) count_tokens_kernel(const PolicyArgs
     a.counts[blockIdx.x] = total;
 }
 
-// Tokens that count, one number a sequence ("sequence_mean"): kLanes threads a
-// sequence, a warp for short ones and a block for long ones.
-template <int kLanes>
-__global__ void __launch_bounds__(kThreads) count_sequences_kernel(const PolicyArgs a) {
-  allow_next();
-  if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
-  const int lane = threadIdx.x % kLanes;
-  const long long teams = static_cast<long long>(gridDim.x) * (kThreads / kLanes);
-  for (long long s = static_cast<long long>(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
-       s < a.t.S; s += teams) {
-    const long long first = sequence_first(a.t, s), len = sequence_end(a.t, s, first) - first;
-    const long long base = a.t.cu != nullptr ? first : s * a.t.ld_mask;
-    // groups begin where the mask is aligned: up to three tokens before the sequence
-    const long long shift = a.vec_mask ? base & 3 : 0;
-    long long n = 0;
-    for (long long c = 4ll * lane - shift; c < len; c += 4 * kLanes) {
-      unsigned range = 15u;
-      if (c < 0) range = 15u << -c & 15u;
-      if (len - c < 4) range &= (1u << (len - c)) - 1u;
-      n += __popc(mask4(a.t, base + c, range, a.vec_mask && range == 15u));
-    }
-    if (kLanes == 32) {
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    } else {
-      n = block_total(n);
-    }
-    if (lane == 0 && store_allowed(a.counts + s, 8, a.r_ws, a.status)) a.counts[s] = n;
-  }
-}
-
 // The weight of a token under "sum" and "mean", and the batch's tokens that
 // count ("mean" only).
 __device__ __forceinline__ float batch_weight(const PolicyArgs& a) {
   if (a.reduction != FLCE_TOKEN_MEAN) return 1.f;
   long long tokens = 0;
-  if (a.num_counts > 0) {
-    for (int i = threadIdx.x; i < a.num_counts; i += kThreads) tokens += a.counts[i];
-    tokens = block_total(tokens);
+  if (a.num_counts > 0) {   // each warp by itself, without a barrier
+    for (int i = threadIdx.x & 31; i < a.num_counts; i += 32) tokens += a.counts[i];
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) tokens += shuffle_xor(tokens, o);
   } else {   // without a mask: what lies in sequences
     tokens = a.t.cu == nullptr ? a.t.N
              : a.t.S > 0 ? max(0ll, clamp_to(a.t.cu[a.t.S], a.t.N) - clamp_to(a.t.cu[0], a.t.N)) : 0;
@@ -587,7 +559,7 @@ __device__ __forceinline__ float batch_weight(const PolicyArgs& a) {
 // The sequence that a thread is in: its advantage and weight.
 struct Sequence {
   Walker w;
-  long long have = -1;
+  int have = -1;
   float adv = 0.f, weight;
   __device__ __forceinline__ explicit Sequence(float batch) : weight(batch) {}
   __device__ __forceinline__ void enter(const PolicyArgs& a) {
@@ -644,7 +616,7 @@ __global__ void __launch_bounds__(kThreads) policy_kernel(const PolicyArgs a) {
     if (g.bits != 0) {
       float x[4], old[4], ref[4] = {}, adv[4], weights[4];
       policy_load<T>(a, g, x, old, ref, adv);
-      if (!kFlat) seq.w.s = g.row;
+      if (!kFlat) seq.w.s = static_cast<int>(g.row);
       if (!kFlat && need_row) seq.enter(a);
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
@@ -720,6 +692,40 @@ __device__ __forceinline__ void store_octet(float* p, unsigned range, const floa
     if (has(range, k) && store_allowed(p + k, 4, r, status)) p[k] = x[k];
 }
 
+// Tokens that count, one number a sequence ("sequence_mean"): kLanes threads a
+// sequence, a warp for short ones and a block for long ones.
+template <int kLanes>
+__global__ void __launch_bounds__(kThreads) count_sequences_kernel(const PolicyArgs a) {
+  allow_next();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
+  const int lane = threadIdx.x % kLanes;
+  const long long teams = static_cast<long long>(gridDim.x) * (kThreads / kLanes);
+  for (long long s = static_cast<long long>(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
+       s < a.t.S; s += teams) {
+    const long long first = sequence_first(a.t, s), len = sequence_end(a.t, s, first) - first;
+    const long long base = a.t.cu != nullptr ? first : s * a.t.ld_mask;
+    // octets begin where the mask is aligned: up to seven tokens before the sequence
+    const bool bytes = a.t.mask_kind == FLCE_MASK_BYTES;
+    const int shift = bytes ? static_cast<int>((reinterpret_cast<uintptr_t>(a.t.mask) + base) & 7u) : 0;
+    long long n = 0;
+#pragma unroll 4
+    for (long long c = 8ll * lane - shift; c < len; c += 8 * kLanes) {
+      const unsigned range = c >= 0 && c + 8 <= len
+                                 ? kWhole
+                                 : tokens_from_to(static_cast<int>(max(0ll, -c)),
+                                                  static_cast<int>(min(8ll, len - c)));
+      n += __popc(mask8(a.t, base + c, range, bytes && range == kWhole));
+    }
+    if (kLanes == 32) {
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    } else {
+      n = block_total(n);
+    }
+    if (lane == 0 && store_allowed(a.counts + s, 8, a.r_ws, a.status)) a.counts[s] = n;
+  }
+}
+
 // One octet of the contiguous streaming kernel. `at` is its first token; `set`
 // of it counts. kRow: its tokens' sequences matter (an advantage or a weight
 // for each).
@@ -748,8 +754,12 @@ struct Octet {
 #pragma unroll
         for (int k = 0; k < 8; ++k) old[k] = a.sign * x[k];
       }
+      if (kRow) {
+        seq.w.to(a.t, at);
+        seq.enter(a);
+      }
       const bool several = kRow && at + 7 >= seq.w.end;   // perhaps several sequences
-      Sequence again = seq;
+      const int before = seq.w.s;
       if (kRow && !a.adv_per_token) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) adv[k] = seq.adv;
@@ -770,15 +780,17 @@ struct Octet {
       policy_tokens(a, x, old, ref, adv, gain, slope, v);
       v.tokens += __popc(set);
       if (kRow && several && a.reduction == FLCE_SEQUENCE_MEAN) {
+        // through the sequences again, now for the weights
+        seq.w.s = before;
+        seq.w.end = -1;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
           if (!has(set, k)) continue;
-          again.w.to(a.t, at + k);
-          again.enter(a);
-          sum = fmaf(gain[k], again.weight, sum);
-          out[k] = slope[k] * (-a.sign * again.weight);
+          seq.w.to(a.t, at + k);
+          seq.enter(a);
+          sum = fmaf(gain[k], seq.weight, sum);
+          out[k] = slope[k] * (-a.sign * seq.weight);
         }
-        seq = again;
       } else {
         const float w = -a.sign * seq.weight;
 #pragma unroll
@@ -798,13 +810,17 @@ struct Octet {
   }
 };
 
-// The streaming kernel of contiguous, aligned batches: a.per octets a block,
-// kThreads at a time, the masks of the next ones on their way; the last few
-// tokens are the last block's.
+// The streaming kernel of contiguous, aligned batches, a.per octets a block,
+// kThreads at a time; the last few tokens are the last block's. Every block takes
+// octets from all over the batch, so that what is masked spreads over the
+// blocks; but where sequences have to be looked up in cu_seqlens a block's
+// octets are one stretch, in which walking on from one to the next is cheap.
 template <typename T, bool kRow>
 __global__ void __launch_bounds__(kThreads, kPolicyBlocksPerSm) policy_octets_kernel(const PolicyArgs a) {
-  const long long octets = a.t.N / 8, o0 = blockIdx.x * a.per;
-  const int count = static_cast<int>(min(octets - o0, a.per));
+  const long long octets = a.t.N / 8;
+  const bool stretch = kRow && a.t.cu != nullptr;
+  const long long stop = stretch ? min(octets, (blockIdx.x + 1) * a.per) : octets;
+  const long long step = stretch ? kThreads : static_cast<long long>(gridDim.x) * kThreads;
   const bool masked = a.t.mask_kind != FLCE_MASK_NONE;
   // the tokens that lie in sequences
   long long first = 0, end = a.t.N;
@@ -816,31 +832,31 @@ __global__ void __launch_bounds__(kThreads, kPolicyBlocksPerSm) policy_octets_ke
     return tokens_from_to(static_cast<int>(min(max(first - at, 0ll), 8ll)),
                           static_cast<int>(min(max(end - at, 0ll), 8ll)));
   };
-  const bool inside = first <= o0 * 8 && (o0 + count) * 8 <= end;   // all of the block's
-  int i = threadIdx.x;
-  unsigned next = kWhole;   // what counts of octet i + kThreads, then of those after it
+  const bool inside = first == 0 && end == a.t.N;   // all tokens do
+  long long i = blockIdx.x * (stretch ? a.per : static_cast<long long>(kThreads)) + threadIdx.x;
+  unsigned next = kWhole;   // what counts of the octet after this one
   Octet<T, kRow> o;
-  // the octet i, whose tokens that count are `set`
+  // octet i, whose tokens that count are `set`
   const auto read = [&](unsigned set) {
-    o.at = (o0 + i) * 8;
+    o.at = i * 8;
     o.set = inside ? set : set & in_sequences(o.at);
     o.template read<true>(a);
   };
-  if (i < count) {
+  if (i < stop) {
     unsigned set = kWhole;
-    if (masked) set = mask8(a.t, (o0 + i) * 8, kWhole, true);
-    if (masked && i + kThreads < count) next = mask8(a.t, (o0 + i + kThreads) * 8, kWhole, true);
+    if (masked) set = mask8(a.t, i * 8, kWhole, true);
+    if (masked && i + step < stop) next = mask8(a.t, (i + step) * 8, kWhole, true);
     read(set);
   }
   wait_for_previous();   // up to here only the caller's tensors were read
   Sequence seq(batch_weight(a));
   Running v{};
-  while (i < count) {
+  while (i < stop) {
     o.template step<true>(a, kWhole, seq, v);
-    i += kThreads;
-    if (i >= count) break;
+    i += step;
+    if (i >= stop) break;
     const unsigned set = next;
-    if (masked && i + kThreads < count) next = mask8(a.t, (o0 + i + kThreads) * 8, kWhole, true);
+    if (masked && i + step < stop) next = mask8(a.t, (i + step) * 8, kWhole, true);
     read(set);
   }
   const int tail = static_cast<int>(a.t.N - octets * 8);

@@ -310,7 +310,7 @@ int flce_policy_loss(const flce_policy_args* a, flce_stream_t stream) {
   k.partials = reinterpret_cast<PolicyPartial*>(ws + L.partials_at);
   if (L.counts > 0) {
     const int64_t work = a->reduction == FLCE_SEQUENCE_MEAN ? t.sequences : (L.groups + 1023) / 1024;
-    const int blocks = static_cast<int>(std::min<int64_t>(work, most));
+    const int blocks = static_cast<int>(std::min<int64_t>(work, kMaxBlocks));
     if (a->reduction == FLCE_TOKEN_MEAN) k.num_counts = blocks;
     v = run_kernel("flce_policy_count", st, [&] { return launch_count(k, blocks, st); });
     if (v != FLCE_OK) return v;

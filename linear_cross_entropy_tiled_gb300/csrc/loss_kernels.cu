@@ -1075,7 +1075,7 @@ __device__ __forceinline__ float preference_pair(const PreferenceArgs& a, long l
       dz = e - 1.f / (1.f + expf(z));
     } else if (a.type == FLCE_PREF_HINGE) {
       loss = isnan(z) ? z : fmaxf(0.f, 1.f - z);
-      dz = z < 1.f ? -1.f : 0.f;
+      dz = isnan(z) ? z : (z < 1.f ? -1.f : 0.f);
     } else {
       const float u = (z - 0.5f) / a.beta;
       loss = u * u;

@@ -8,6 +8,7 @@
 #include <cmath>
 
 #include "flce.h"
+#include "nvtx_range.h"
 #include "post_training.h"
 
 using namespace flce;
@@ -220,6 +221,7 @@ int flce_policy_workspace_bytes(const flce_policy_args* a, size_t* bytes) {
 }
 
 int flce_policy_loss(const flce_policy_args* a, flce_stream_t stream) {
+  NvtxRange range("flce_policy_loss");
   int v = check_policy(a);
   if (v != FLCE_OK) return v;
   const flce_tokens& t = a->tokens;
@@ -301,9 +303,11 @@ int flce_policy_loss(const flce_policy_args* a, flce_stream_t stream) {
   }
   const int64_t most = std::min<int64_t>(kMaxBlocks, int64_t(sms) * kPolicyBlocksPerSm);
   const int64_t units = k.octets ? token_total(t) / 8 : L.groups;
-  k.per = (units + most - 1) / most;
-  k.per = (k.per + 255) / 256 * 256;   // whole rounds of a block's threads
-  const unsigned grid = static_cast<unsigned>((units + k.per - 1) / k.per);
+  // Whole rounds of a block's threads; one block at least, also for a batch of
+  // many sequences but few tokens or none.
+  k.per = std::max<int64_t>(1, (units + most - 1) / most);
+  k.per = (k.per + 255) / 256 * 256;
+  const unsigned grid = static_cast<unsigned>(std::max<int64_t>(1, (units + k.per - 1) / k.per));
   k.done = reinterpret_cast<int*>(ws);
   k.counts = reinterpret_cast<long long*>(ws + L.counts_at);
   k.num_counts = L.counts;
@@ -332,6 +336,7 @@ int flce_preference_workspace_bytes(const flce_preference_args* a, size_t* bytes
 }
 
 int flce_preference_loss(const flce_preference_args* a, flce_stream_t stream) {
+  NvtxRange range("flce_preference_loss");
   int v = check_preference(a);
   if (v != FLCE_OK) return v;
   const flce_tokens& t = a->tokens;
@@ -403,6 +408,7 @@ int flce_preference_loss(const flce_preference_args* a, flce_stream_t stream) {
 }
 
 int flce_adamw(const flce_adamw_args* a, flce_stream_t stream) {
+  NvtxRange range("flce_adamw");
   if (a == nullptr) return refuse(FLCE_ERR_INVALID_ARG, "arguments are NULL");
   if (a->count < 0 || a->count > (int64_t(1) << 30) || (a->count > 0 && a->tensors == nullptr))
     return refuse(FLCE_ERR_INVALID_ARG, "tensors or count");

@@ -172,35 +172,45 @@ class AdamW(torch.optim.Optimizer):
     ``state_bits``: 32, or 8 for e4m3 states with a scale for each 256
     elements (about 2 bytes a parameter instead of 8). ``master_weights``
     keeps a float32 copy of 16-bit parameters, which takes the updates.
-    ``seed`` picks the random bits of 8-bit states. ``step(grad_scale=...)``
-    takes a float32 device scalar that multiplies every gradient.
+    ``seed`` picks the random bits of 8-bit states. All of them can differ
+    between parameter groups. ``step(grad_scale=...)`` takes a float32 device
+    scalar that multiplies every gradient.
     """
 
     def __init__(self, params, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay: float = 0.01, *, state_bits: int = 32, master_weights: bool = False,
                  seed: int = 0):
-        if state_bits not in (8, 32):
-            raise ValueError(f"state_bits must be 8 or 32, got {state_bits}")
-        for name, x in (("lr", lr), ("eps", eps), ("weight_decay", weight_decay)):
-            if not 0.0 <= x < float("inf"):
-                raise ValueError(f"{name} must be finite and not negative, got {x}")
-        if not all(0.0 <= b < 1.0 for b in betas):
-            raise ValueError(f"betas must be in [0, 1), got {betas}")
-        self._bits, self._master, self._seed = state_bits, bool(master_weights), int(seed)
+        defaults = dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay, state_bits=state_bits,
+                        master_weights=bool(master_weights), seed=int(seed))
         self._plans: dict = {}
-        super().__init__(params, dict(lr=lr, betas=betas, eps=eps, weight_decay=weight_decay))
+        super().__init__(params, defaults)
 
-    def _init_state(self, p: torch.Tensor) -> dict:
-        s = self.state[p]
-        dt = torch.float8_e4m3fn if self._bits == 8 else torch.float32
+    def add_param_group(self, param_group: dict) -> None:
+        g = {**self.defaults, **param_group}
+        if g["state_bits"] not in (8, 32):
+            raise ValueError(f"state_bits must be 8 or 32, got {g['state_bits']}")
+        for name in ("lr", "eps", "weight_decay"):
+            if not 0.0 <= g[name] < float("inf"):
+                raise ValueError(f"{name} must be finite and not negative, got {g[name]}")
+        if not all(0.0 <= b < 1.0 for b in g["betas"]):
+            raise ValueError(f"betas must be in [0, 1), got {g['betas']}")
+        super().add_param_group(param_group)
+
+    def __setstate__(self, state: dict) -> None:
+        super().__setstate__(state)
+        self._plans = {}
+
+    def _init_state(self, p: torch.Tensor, group: dict) -> dict:
+        s, bits = self.state[p], group["state_bits"]
+        dt = torch.float8_e4m3fn if bits == 8 else torch.float32
         s["step"] = 0
         for k in ("exp_avg", "exp_avg_sq"):
             z = torch.empty_strided(p.shape, p.stride(), dtype=dt, device=p.device)
-            (z.view(torch.uint8) if self._bits == 8 else z).zero_()
+            (z.view(torch.uint8) if bits == 8 else z).zero_()
             s[k] = z
-            if self._bits == 8:
+            if bits == 8:
                 s[k + "_scale"] = torch.zeros(-(-p.numel() // BLOCK), device=p.device)
-        if self._master and p.dtype != torch.float32:
+        if group["master_weights"] and p.dtype != torch.float32:
             s["master"] = torch.empty_strided(p.shape, p.stride(), dtype=torch.float32,
                                               device=p.device).copy_(p.detach())
         return s
@@ -237,14 +247,14 @@ class AdamW(torch.optim.Optimizer):
                     raise RuntimeError("AdamW does not take sparse gradients")
                 s = self.state[p]
                 if not s:
-                    s = self._init_state(p)
+                    s = self._init_state(p, group)
                 s["step"] += 1
                 batches.setdefault((p.dtype, p.device, p.grad.dtype, s["step"]), []).append(p)
             for (_, _, _, t), params in batches.items():
                 self._plan(params).step([p.grad for p in params], step=t, lr=float(group["lr"]),
                                         betas=group["betas"], eps=group["eps"],
                                         weight_decay=group["weight_decay"], grad_scale=grad_scale,
-                                        seed=self._seed)
+                                        seed=group["seed"])
         return loss
 
     def load_state_dict(self, state_dict: dict) -> None:

@@ -21,6 +21,8 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "elements.cuh"
 #include "post_training.h"
 #include "ptx.cuh"
@@ -143,6 +145,13 @@ __device__ __forceinline__ unsigned nonzero_bytes(unsigned w) {
   return (((w & 0x7f7f7f7fu) + 0x7f7f7f7fu) | w) & 0x80808080u;
 }
 
+// How many of 16 bytes are not 0: their top bits moved apart, so that one
+// population count does for all.
+__device__ __forceinline__ int count_bytes(const uint4& w) {
+  return __popc(nonzero_bytes(w.x) | nonzero_bytes(w.y) >> 1 | nonzero_bytes(w.z) >> 2 |
+                nonzero_bytes(w.w) >> 3);
+}
+
 // Which of the tokens i .. i + 3 of the mask (of those in `range`) count.
 __device__ __forceinline__ unsigned mask4(const TokenView& t, long long i, unsigned range, bool vec) {
   if (t.mask_kind == FLCE_MASK_NONE) return range;
@@ -182,6 +191,21 @@ __device__ __forceinline__ long long sequence_end(const TokenView& t, long long 
 struct Walker {
   int s = 0;
   long long end = -1;
+  // For a whole warp, packed: to the sequence of the first lane's token i, 32
+  // at a time, so that `to` has only the warp's own tokens left to walk.
+  __device__ __forceinline__ void start(const TokenView& t, long long i) {
+    i = __shfl_sync(0xffffffffu, i, 0);
+    const int lane = threadIdx.x & 31;
+    long long lo = 0, hi = t.S;   // the last sequence that begins at or before i is in [lo, hi)
+    while (hi - lo > 1) {
+      const long long part = (hi - lo + 31) / 32, at = lo + lane * part;
+      const int n = __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(t.cu + at) <= i));
+      if (n > 0) lo += (n - 1) * part;
+      hi = n == 0 ? lo : min(hi, lo + part);
+    }
+    s = static_cast<int>(lo);
+    end = -1;
+  }
   __device__ __forceinline__ void to(const TokenView& t, long long i) {
     if (i < end) return;
     if (t.cu == nullptr) {
@@ -517,12 +541,7 @@ __global__ void __launch_bounds__(kThreads) count_tokens_kernel(const PolicyArgs
     const long long from = min(end, first + (off == 0 ? 0 : 16 - off)), vectors = (end - from) / 16;
     const uint4* v = reinterpret_cast<const uint4*>(m + from);
 #pragma unroll 4
-    for (long long i = me; i < vectors; i += step) {
-      const uint4 w = __ldg(v + i);
-      // one bit a byte, moved apart, so that one population count does for all four
-      n += __popc(nonzero_bytes(w.x) | nonzero_bytes(w.y) >> 1 | nonzero_bytes(w.z) >> 2 |
-                  nonzero_bytes(w.w) >> 3);
-    }
+    for (long long i = me; i < vectors; i += step) n += count_bytes(__ldg(v + i));
     if (blockIdx.x == 0) {
       const long long behind = from + vectors * 16;
       if (threadIdx.x < from - first) n += m[first + threadIdx.x] != 0 ? 1 : 0;
@@ -693,35 +712,35 @@ __device__ __forceinline__ void store_octet(float* p, unsigned range, const floa
 }
 
 // Tokens that count, one number a sequence ("sequence_mean"): kLanes threads a
-// sequence, a warp for short ones and a block for long ones.
+// sequence, a warp for short ones and a block for long ones. Bytes are read
+// sixteen at a time where they are aligned, which begins `head` bytes into the
+// sequence.
 template <int kLanes>
-__global__ void __launch_bounds__(kThreads) count_sequences_kernel(const PolicyArgs a) {
+__global__ void __launch_bounds__(kLanes == 32 ? kThreads : kLanes) count_sequences_kernel(const PolicyArgs a) {
+  constexpr int kTeams = kLanes == 32 ? kThreads / 32 : 1;
   allow_next();
   if (blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0;
   const int lane = threadIdx.x % kLanes;
-  const long long teams = static_cast<long long>(gridDim.x) * (kThreads / kLanes);
-  for (long long s = static_cast<long long>(blockIdx.x) * (kThreads / kLanes) + threadIdx.x / kLanes;
-       s < a.t.S; s += teams) {
+  for (long long s = static_cast<long long>(blockIdx.x) * kTeams + threadIdx.x / kLanes; s < a.t.S;
+       s += static_cast<long long>(gridDim.x) * kTeams) {
     const long long first = sequence_first(a.t, s), len = sequence_end(a.t, s, first) - first;
     const long long base = a.t.cu != nullptr ? first : s * a.t.ld_mask;
-    // octets begin where the mask is aligned: up to seven tokens before the sequence
-    const bool bytes = a.t.mask_kind == FLCE_MASK_BYTES;
-    const int shift = bytes ? static_cast<int>((reinterpret_cast<uintptr_t>(a.t.mask) + base) & 7u) : 0;
-    long long n = 0;
+    int n = 0;
+    if (a.t.mask_kind == FLCE_MASK_BYTES) {
+      const unsigned char* m = static_cast<const unsigned char*>(a.t.mask) + base;
+      const long long head = min(len, static_cast<long long>(-reinterpret_cast<uintptr_t>(m) & 15u));
+      const long long vectors = (len - head) / 16, tail = head + vectors * 16;
+      const uint4* v = reinterpret_cast<const uint4*>(m + head);
 #pragma unroll 4
-    for (long long c = 8ll * lane - shift; c < len; c += 8 * kLanes) {
-      const unsigned range = c >= 0 && c + 8 <= len
-                                 ? kWhole
-                                 : tokens_from_to(static_cast<int>(max(0ll, -c)),
-                                                  static_cast<int>(min(8ll, len - c)));
-      n += __popc(mask8(a.t, base + c, range, bytes && range == kWhole));
-    }
-    if (kLanes == 32) {
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      for (long long c = lane; c < vectors; c += kLanes) n += count_bytes(__ldg(v + c));
+      if (lane < head) n += m[lane] != 0 ? 1 : 0;
+      if (lane < len - tail) n += m[tail + lane] != 0 ? 1 : 0;
     } else {
-      n = block_total(n);
+      const long long* m = static_cast<const long long*>(a.t.mask) + base;
+#pragma unroll 4
+      for (long long c = lane; c < len; c += kLanes) n += __ldg(m + c) != a.t.ignore_index ? 1 : 0;
     }
+    n = kLanes == 32 ? __reduce_add_sync(0xffffffffu, n) : block_total(n);
     if (lane == 0 && store_allowed(a.counts + s, 8, a.r_ws, a.status)) a.counts[s] = n;
   }
 }
@@ -760,18 +779,23 @@ struct Octet {
       }
       const bool several = kRow && at + 7 >= seq.w.end;   // perhaps several sequences
       const int before = seq.w.s;
+      // each(f): f(from) for every sequence of the octet, which begins at its
+      // token `from`; seq is in it
+      const auto each = [&](auto f) {
+        for (long long pos = at; pos < at + 8; pos = max(pos + 1, seq.w.end)) {
+          seq.w.to(a.t, pos);
+          seq.enter(a);
+          f(static_cast<int>(pos - at));
+        }
+      };
       if (kRow && !a.adv_per_token) {
 #pragma unroll
         for (int k = 0; k < 8; ++k) adv[k] = seq.adv;
-        if (several) {
+        if (several)
+          each([&](int from) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            if (!has(set, k)) continue;
-            seq.w.to(a.t, at + k);
-            seq.enter(a);
-            adv[k] = seq.adv;
-          }
-        }
+            for (int k = 0; k < 8; ++k) adv[k] = k >= from ? seq.adv : adv[k];
+          });
       }
       if (set != kWhole) {
 #pragma unroll
@@ -781,15 +805,18 @@ struct Octet {
       v.tokens += __popc(set);
       if (kRow && several && a.reduction == FLCE_SEQUENCE_MEAN) {
         // through the sequences again, now for the weights
+        float weights[8] = {};
         seq.w.s = before;
         seq.w.end = -1;
+        each([&](int from) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) weights[k] = k >= from ? seq.weight : weights[k];
+        });
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-          if (!has(set, k)) continue;
-          seq.w.to(a.t, at + k);
-          seq.enter(a);
-          sum = fmaf(gain[k], seq.weight, sum);
-          out[k] = slope[k] * (-a.sign * seq.weight);
+          // a token that does not count has gain 0, but may have a slope (k1)
+          sum = fmaf(gain[k], weights[k], sum);
+          out[k] = has(set, k) ? slope[k] * (-a.sign * weights[k]) : 0.f;
         }
       } else {
         const float w = -a.sign * seq.weight;
@@ -842,6 +869,8 @@ __global__ void __launch_bounds__(kThreads, kPolicyBlocksPerSm) policy_octets_ke
     o.set = inside ? set : set & in_sequences(o.at);
     o.template read<true>(a);
   };
+  Sequence seq(1.f);
+  if (stretch) seq.w.start(a.t, i * 8);
   if (i < stop) {
     unsigned set = kWhole;
     if (masked) set = mask8(a.t, i * 8, kWhole, true);
@@ -849,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, kPolicyBlocksPerSm) policy_octets_ke
     read(set);
   }
   wait_for_previous();   // up to here only the caller's tensors were read
-  Sequence seq(batch_weight(a));
+  seq.weight = batch_weight(a);
   Running v{};
   while (i < stop) {
     o.template step<true>(a, kWhole, seq, v);
@@ -949,7 +978,10 @@ __device__ __forceinline__ PairPart warp_sum(PairPart v) {
   return v;
 }
 
-// A team that is one block, and one that is a cluster.
+// A team that is a warp, one that is a block, and one that is a cluster.
+struct WarpTeam {
+  __device__ __forceinline__ PairPart get(const PairPart& own) const { return own; }
+};
 struct BlockTeam {
   __device__ __forceinline__ void operator()(PairPart&) const { __syncwarp(); }
   __device__ __forceinline__ PairPart get(const PairPart& own) const { return own; }
@@ -1043,24 +1075,11 @@ __device__ __forceinline__ float preference_pair(const PreferenceArgs& a, long l
     n_c += side_c ? __popc(edge_set) : 0;
     n_r += side_c ? 0 : __popc(edge_set);
   }
-  // Sums and counts over the team. Warps first, then the first warp of a block
+  // Sums and counts over the team: warps first, then the first warp of a block
   // over its warps, which also does the pair's arithmetic: with every warp
   // doing all of it, it was most of the instructions of a batch of 8192 a row.
-  __shared__ PairPart s_warp[kPairThreads / 32];
-  __shared__ PairPart s_block;
-  __shared__ float s_out[3];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  PairPart part{sum_c.total(), sum_r.total(), n_c, n_r};
-  part = warp_sum(part);
-  if (lane == 0) s_warp[warp] = part;
-  __syncthreads();
-  if (warp == 0) {
-    part = warp_sum(lane < kPairThreads / 32 ? s_warp[lane] : PairPart{});
-    if (lane == 0) s_block = part;
-  }
-  total(s_block);
-  if (warp == 0) {
-    const PairPart p = total.get(s_block);
+  float w_c = 0.f, w_r = 0.f, loss = 0.f;
+  const auto arithmetic = [&](const PairPart& p) {
     float inv_c = 1.f, inv_r = 1.f;
     if (a.average) {
       inv_c = 1.f / static_cast<float>(max(1, p.n_c));
@@ -1068,7 +1087,7 @@ __device__ __forceinline__ float preference_pair(const PreferenceArgs& a, long l
     }
     const float s_c = p.c * inv_c, s_r = p.r * inv_r;
     const float e = a.smoothing, z = a.beta * (s_c - s_r) - a.margin;
-    float loss, dz;
+    float dz;
     if (a.type == FLCE_PREF_SIGMOID) {
       const float soft = log1pf(expf(-fabsf(z)));
       loss = isnan(z) ? z : (1.f - e) * (soft + fmaxf(-z, 0.f)) + e * (soft + fmaxf(z, 0.f));
@@ -1086,14 +1105,37 @@ __device__ __forceinline__ float preference_pair(const PreferenceArgs& a, long l
       if (a.rejected != nullptr) a.rejected[b] = a.beta * s_r;
     }
     const float g = a.sign * a.beta * dz / static_cast<float>(pairs);
-    if (lane == 0) {
-      s_out[0] = g * inv_c;
-      s_out[1] = -g * inv_r;
-      s_out[2] = loss;
+    w_c = g * inv_c;
+    w_r = -g * inv_r;
+  };
+  PairPart part = warp_sum(PairPart{sum_c.total(), sum_r.total(), n_c, n_r});
+  if constexpr (std::is_same<Total, WarpTeam>::value) {
+    arithmetic(part);
+  } else {
+    __shared__ PairPart s_warp[kPairThreads / 32];
+    __shared__ PairPart s_block;
+    __shared__ float s_out[3];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (lane == 0) s_warp[warp] = part;
+    __syncthreads();
+    if (warp == 0) {
+      part = warp_sum(lane < kPairThreads / 32 ? s_warp[lane] : PairPart{});
+      if (lane == 0) s_block = part;
     }
+    total(s_block);
+    if (warp == 0) {
+      arithmetic(total.get(s_block));
+      if (lane == 0) {
+        s_out[0] = w_c;
+        s_out[1] = w_r;
+        s_out[2] = loss;
+      }
+    }
+    __syncthreads();
+    w_c = s_out[0];
+    w_r = s_out[1];
+    loss = s_out[2];
   }
-  __syncthreads();
-  const float w_c = s_out[0], w_r = s_out[1], loss = s_out[2];
   if (a.grad == nullptr) return loss;
   for (int j = member; j < whole; j += kKept * team) {
     unsigned long long sets = j == member ? kept : sets_from(j);
@@ -1110,8 +1152,20 @@ __device__ __forceinline__ float preference_pair(const PreferenceArgs& a, long l
   return loss;
 }
 
-// A cluster takes a pair (kSeveral: it has more than one block); the last block to
-// finish averages the pairs' losses.
+// The last block to finish averages the pairs' losses. `expected`: the shares
+// that are counted, this one by thread 0 if `counts`.
+__device__ __forceinline__ void preference_finish(const PreferenceArgs& a, bool counts, int expected) {
+  __shared__ bool s_last;
+  if (threadIdx.x == 0) s_last = counts && counted_last(a.done, expected);
+  __syncthreads();
+  if (!s_last) return;
+  Sum sum{};
+  for (long long i = threadIdx.x; i < a.t.S / 2; i += kPairThreads) sum.add(__ldcg(a.pair_loss + i));
+  sum = block_total(sum);
+  if (threadIdx.x == 0) *a.loss = sum.total() / static_cast<float>(a.t.S / 2);
+}
+
+// A cluster takes a pair (kSeveral: it has more than one block).
 template <typename T, bool kVec, bool kSeveral>
 __global__ void __launch_bounds__(kPairThreads, 4) preference_kernel(const PreferenceArgs a) {
   int blocks = 1, rank = 0;
@@ -1129,20 +1183,21 @@ __global__ void __launch_bounds__(kPairThreads, 4) preference_kernel(const Prefe
   } else {
     loss = preference_pair<T, kVec>(a, b, member, team, BlockTeam{});
   }
-  __shared__ bool s_last;
-  if (threadIdx.x == 0) {
-    s_last = false;
-    if (rank == 0) {
-      if (store_allowed(a.pair_loss + b, 4, a.r_ws, a.status)) a.pair_loss[b] = loss;
-      s_last = counted_last(a.done, static_cast<int>(a.t.S / 2));
-    }
+  if (rank == 0 && threadIdx.x == 0 && store_allowed(a.pair_loss + b, 4, a.r_ws, a.status))
+    a.pair_loss[b] = loss;
+  preference_finish(a, rank == 0, static_cast<int>(a.t.S / 2));
+}
+
+// A warp takes a pair, of short sequences.
+template <typename T, bool kVec>
+__global__ void __launch_bounds__(kPairThreads) preference_warps_kernel(const PreferenceArgs a) {
+  const long long b = static_cast<long long>(blockIdx.x) * (kPairThreads / 32) + (threadIdx.x >> 5);
+  if (b < a.t.S / 2) {
+    const float loss = preference_pair<T, kVec>(a, b, threadIdx.x & 31, 32, WarpTeam{});
+    if ((threadIdx.x & 31) == 0 && store_allowed(a.pair_loss + b, 4, a.r_ws, a.status)) a.pair_loss[b] = loss;
   }
-  __syncthreads();
-  if (!s_last) return;
-  Sum sum{};
-  for (long long i = threadIdx.x; i < a.t.S / 2; i += kPairThreads) sum.add(__ldcg(a.pair_loss + i));
-  sum = block_total(sum);
-  if (threadIdx.x == 0) *a.loss = sum.total() / static_cast<float>(a.t.S / 2);
+  __syncthreads();   // the block's losses are stored: thread 0's fence publishes them
+  preference_finish(a, true, static_cast<int>(gridDim.x));
 }
 
 // One cluster; its blocks take the pairs in turn.
@@ -1206,7 +1261,7 @@ cudaError_t launch_count(const PolicyArgs& a, int blocks, cudaStream_t s) {
   } else if (a.t.N / (a.t.S > 0 ? a.t.S : 1) < 1024) {
     count_sequences_kernel<32><<<blocks, kThreads, 0, s>>>(a);
   } else {
-    count_sequences_kernel<kThreads><<<blocks, kThreads, 0, s>>>(a);
+    count_sequences_kernel<512><<<blocks, 512, 0, s>>>(a);
   }
   note_launch();
   return cudaGetLastError();
@@ -1246,22 +1301,30 @@ cudaError_t launch_preference_small(const PreferenceArgs& a, int dtype, cudaStre
 }
 
 cudaError_t launch_preference(const PreferenceArgs& a, int dtype, int cluster, cudaStream_t s) {
+  const long long pairs = a.t.S / 2;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr.val.clusterDim.x = static_cast<unsigned>(cluster > 0 ? cluster : 1);
   attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  const unsigned grid = static_cast<unsigned>(a.t.S / 2) * static_cast<unsigned>(cluster);
-  const auto pick = [&](auto* several, auto* one) {
-    return launch_with(attr, grid, kPairThreads, s, cluster > 1 ? several : one, a);
+  constexpr int kWarps = kPairThreads / 32;
+  const unsigned grid = static_cast<unsigned>(cluster > 0 ? pairs * cluster : (pairs + kWarps - 1) / kWarps);
+  const auto pick = [&](auto* several, auto* one, auto* warps) {
+    return launch_with(attr, grid, kPairThreads, s, cluster > 1 ? several : cluster == 1 ? one : warps, a);
   };
   if (dtype == FLCE_BF16)
-    return a.vec ? pick(preference_kernel<__nv_bfloat16, true, true>, preference_kernel<__nv_bfloat16, true, false>)
-                 : pick(preference_kernel<__nv_bfloat16, false, true>, preference_kernel<__nv_bfloat16, false, false>);
+    return a.vec ? pick(preference_kernel<__nv_bfloat16, true, true>, preference_kernel<__nv_bfloat16, true, false>,
+                        preference_warps_kernel<__nv_bfloat16, true>)
+                 : pick(preference_kernel<__nv_bfloat16, false, true>, preference_kernel<__nv_bfloat16, false, false>,
+                        preference_warps_kernel<__nv_bfloat16, false>);
   if (dtype == FLCE_F16)
-    return a.vec ? pick(preference_kernel<__half, true, true>, preference_kernel<__half, true, false>)
-                 : pick(preference_kernel<__half, false, true>, preference_kernel<__half, false, false>);
-  return a.vec ? pick(preference_kernel<float, true, true>, preference_kernel<float, true, false>)
-               : pick(preference_kernel<float, false, true>, preference_kernel<float, false, false>);
+    return a.vec ? pick(preference_kernel<__half, true, true>, preference_kernel<__half, true, false>,
+                        preference_warps_kernel<__half, true>)
+                 : pick(preference_kernel<__half, false, true>, preference_kernel<__half, false, false>,
+                        preference_warps_kernel<__half, false>);
+  return a.vec ? pick(preference_kernel<float, true, true>, preference_kernel<float, true, false>,
+                      preference_warps_kernel<float, true>)
+               : pick(preference_kernel<float, false, true>, preference_kernel<float, false, false>,
+                      preference_warps_kernel<float, false>);
 }
 
 }  // namespace flce

@@ -399,8 +399,9 @@ int flce_preference_loss(const flce_preference_args* a, flce_stream_t stream) {
   // Blocks a pair: enough for two on each SM, while each still has 4096 tokens.
   // (512 pairs of 2 x 8192 tokens: 26 us with one block a pair, 32 us with two.)
   const int64_t a_pair = token_total(t) / pairs;
-  int cluster = 1;
-  while (cluster < 8 && pairs * cluster < 2 * sms && a_pair / (cluster * 2) >= 4096) cluster *= 2;
+  // Where there are many pairs of few tokens a warp takes one (cluster 0).
+  int cluster = a_pair <= kWarpPairTokens && pairs >= 4 * sms ? 0 : 1;
+  while (cluster > 0 && cluster < 8 && pairs * cluster < 2 * sms && a_pair / (cluster * 2) >= 4096) cluster *= 2;
   const cudaError_t e = cudaMemsetAsync(k.done, 0, sizeof(int), st);
   if (e != cudaSuccess) return cuda_error(e, "cudaMemsetAsync");
   v = run_kernel("flce_preference", st, [&] { return launch_preference(k, a->dtype, cluster, st); });

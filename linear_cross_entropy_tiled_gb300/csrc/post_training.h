@@ -79,6 +79,10 @@ struct PolicyArgs {
 
 constexpr long long kPreferenceSmallTokens = 65536;
 constexpr long long kPreferenceSmallPairs = 64;
+// Tokens of a pair up to which a warp takes it. On the GPU, a call of 4096 pairs
+// of 2 x 300 tokens: 15 us, 41 us with a block a pair; of 1000 pairs of
+// 2 x 2000: 32 us, 21 us with a block a pair.
+constexpr long long kWarpPairTokens = 1024;
 
 struct PreferenceArgs {
   TokenView t;
@@ -105,7 +109,7 @@ cudaError_t launch_count(const PolicyArgs& a, int blocks, cudaStream_t s);
 // after_count: launch_count is the kernel right before it in the stream.
 cudaError_t launch_policy(const PolicyArgs& a, int dtype, bool after_count, unsigned grid, cudaStream_t s);
 cudaError_t launch_preference_small(const PreferenceArgs& a, int dtype, cudaStream_t s);
-// cluster: blocks a pair (1, 2, 4 or 8).
+// cluster: blocks a pair (1, 2, 4 or 8), or 0: a warp a pair.
 cudaError_t launch_preference(const PreferenceArgs& a, int dtype, int cluster, cudaStream_t s);
 
 struct AdamWArgs {

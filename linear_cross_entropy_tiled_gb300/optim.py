@@ -209,10 +209,9 @@ class AdamW(torch.optim.Optimizer):
                                               device=p.device).copy_(p.detach())
         return s
 
-    def _plan(self, params: list) -> _Plan:
+    def _plan(self, params: list, states: list) -> _Plan:
         # A plan is kept while every tensor in it stays as it is in memory. It
         # holds them, so none of their memory can come back as another tensor.
-        states = [self.state[p] for p in params]
         names = [k for k in ("exp_avg", "exp_avg_sq", "exp_avg_scale", "exp_avg_sq_scale", "master")
                  if k in states[0]]
         lists = {k: [s[k] for s in states] for k in names}
@@ -237,21 +236,28 @@ class AdamW(torch.optim.Optimizer):
         for group in self.param_groups:
             batches: dict = {}
             for p in group["params"]:
-                if p.grad is None:
+                g = p.grad
+                if g is None:
                     continue
-                if p.grad.is_sparse:
+                if g.is_sparse:
                     raise RuntimeError("AdamW does not take sparse gradients")
                 s = self.state[p]
                 if not s:
                     s = self._init_state(p, group)
-                batches.setdefault((p.dtype, p.device, p.grad.dtype, s["step"] + 1), []).append(p)
-            for (_, _, _, t), params in batches.items():
-                self._plan(params).step([p.grad for p in params], step=t, lr=float(group["lr"]),
-                                        betas=group["betas"], eps=group["eps"],
-                                        weight_decay=group["weight_decay"], grad_scale=grad_scale,
-                                        seed=group["seed"])
-                for p in params:   # not those of a step that was refused
-                    self.state[p]["step"] = t
+                key = p.dtype, p.device, g.dtype, s["step"] + 1
+                if key not in batches:
+                    batches[key] = [], [], []
+                params, states, grads = batches[key]
+                params.append(p)
+                states.append(s)
+                grads.append(g)
+            for (_, _, _, t), (params, states, grads) in batches.items():
+                self._plan(params, states).step(grads, step=t, lr=float(group["lr"]),
+                                                betas=group["betas"], eps=group["eps"],
+                                                weight_decay=group["weight_decay"],
+                                                grad_scale=grad_scale, seed=group["seed"])
+                for s in states:   # not those of a step that was refused
+                    s["step"] = t
         return loss
 
     def load_state_dict(self, state_dict: dict) -> None:

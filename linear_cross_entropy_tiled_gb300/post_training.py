@@ -23,85 +23,59 @@ from . import _lib
 from .functional import (_DTYPES, _maybe_check, _params, _prepare, _ptr, _stream, flce_backward,
                          flce_forward)
 
-# Workspace bounds of include/flce.h: none for this many tokens, else so many
-# bytes and 8 (preference loss: 4) for each sequence (pair).
-_SMALL = 8192
-_POLICY_WORKSPACE, _PREFERENCE_WORKSPACE = 49152, 256
 
-
-def _laid_out(t: torch.Tensor, shape, dtype, device, name: str):
-    """(tensor, row stride) of a token tensor; anything but adjacent tokens in a row is copied."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must have the shape of the log probabilities, {tuple(shape)}, "
+def _regular(t: torch.Tensor, x: torch.Tensor, dtype, name: str) -> torch.Tensor:
+    """t, or its contiguous copy unless neighbouring tokens of a row are adjacent; it must be like x."""
+    if t.shape != x.shape:
+        raise ValueError(f"{name} must have the shape of the log probabilities, {tuple(x.shape)}, "
                          f"got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}")
-    cols = shape[-1]
-    if t.is_contiguous():
-        return t, cols
-    if len(shape) == 1 or (cols > 1 and t.stride(1) != 1) or t.stride(0) < cols:
-        return t.contiguous(), cols
-    return t, t.stride(0)
+    if t.device != x.device:
+        raise ValueError(f"{name} must be on {x.device}")
+    cols = x.shape[-1]
+    if t.is_contiguous() or (t.dim() == 2 and (cols <= 1 or t.stride(1) == 1) and t.stride(0) >= cols):
+        return t
+    return t.contiguous()
 
 
-def _tokens(x: torch.Tensor, mask, cu_seqlens, name: str):
-    """The fields of flce_tokens, the number of sequences, and the tensors they point to."""
+def _regular_tokens(x, mask, cu_seqlens, ignore_index):
+    """log probs, mask (or labels) and cu_seqlens, checked, and copied where they have to be."""
     if not x.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
+        raise ValueError("log_probs must be a CUDA tensor (there is no CPU path)")
     if x.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be float32, bfloat16 or float16, got {x.dtype}")
-    shape = x.shape
+        raise TypeError(f"log_probs must be float32, bfloat16 or float16, got {x.dtype}")
+    shape = tuple(x.shape)
     if cu_seqlens is None:
         if len(shape) != 2:
-            raise ValueError(f"{name} must be [sequences, cols], or [tokens] with cu_seqlens; "
-                             f"got {tuple(shape)}")
-        sequences, cols = shape
-        tokens = packed = cu = 0
+            raise ValueError("log_probs (targets) must be [sequences, cols], or [tokens] with "
+                             f"cu_seqlens; got {shape}")
     else:
         if len(shape) != 1:
-            raise ValueError(f"{name} must be [tokens] with cu_seqlens, got {tuple(shape)}")
+            raise ValueError(f"log_probs (targets) must be [tokens] with cu_seqlens, got {shape}")
         if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1 or cu_seqlens.device != x.device:
             raise ValueError(f"cu_seqlens must be [sequences + 1] on {x.device}")
         if cu_seqlens.dtype not in (torch.int32, torch.int64):
             raise TypeError(f"cu_seqlens must be int32 or int64, got {cu_seqlens.dtype}")
         cu_seqlens = cu_seqlens.to(torch.int32).contiguous()
-        sequences, cols, tokens, packed = cu_seqlens.shape[0] - 1, 0, shape[0], 1
-        cu = cu_seqlens.data_ptr()
-    where = kind = ld = 0
     if mask is not None:
-        if mask.dtype is not torch.bool and mask.dtype is not torch.uint8:
+        if ignore_index is None and mask.dtype not in (torch.bool, torch.uint8):
             raise TypeError(f"mask must be bool or uint8, got {mask.dtype}")
-        mask, ld = _laid_out(mask, shape, mask.dtype, x.device, "mask")
-        where, kind = mask.data_ptr(), _lib.FLCE_MASK_BYTES
-    return (sequences, cols, tokens, cu, where, ld, 0, packed, kind), sequences, (cu_seqlens, mask)
+        mask = _regular(mask, x, mask.dtype, "mask")
+    return _regular(x, x, x.dtype, "log_probs"), mask, cu_seqlens
 
 
-def _label_tokens(nll, labels, ignore_index, cu_seqlens):
-    """``_tokens`` for log probabilities of ``labels`` (contiguous): those that are ignored do not count."""
-    (sequences, cols, tokens, cu, *_, packed, _), n, keep = _tokens(nll, None, cu_seqlens, "targets")
-    return (sequences, cols, tokens, cu, labels.data_ptr(), labels.shape[-1], ignore_index, packed,
-            _lib.FLCE_MASK_LABELS), n, keep
-
-
-def _float_like(x: torch.Tensor, shape, device) -> torch.Tensor:
-    """A new contiguous float32 tensor of the log probabilities' shape."""
-    if x.dtype is torch.float32 and x.is_contiguous():
-        return torch.empty_like(x)
-    return torch.empty(shape, dtype=torch.float32, device=device)
-
-
-_templates: dict = {}
-
-
-def _scalar_templates(device):
-    """A float32 and an int64 scalar of the device for empty_like, the quickest way to new scalars."""
-    t = _templates.get(device)
-    if t is None:
-        t = _templates[device] = (torch.empty((), dtype=torch.float32, device=device),
-                                  torch.empty((), dtype=torch.int64, device=device))
-    return t
+def _call(fn, entry: str, regular, tensors: tuple, numbers: tuple):
+    """The outputs of a call through flce_tensors, if need be on what ``regular`` makes of the tensors."""
+    x, at = tensors[0], _lib.entry_address(entry)
+    out = fn(at, _stream(x.device), *tensors, *numbers) if x.is_cuda else None
+    if out is None:
+        tensors = regular(*tensors)   # raises where something is wrong
+        out = fn(at, _stream(x.device), *tensors, *numbers)
+        if out is None:
+            raise TypeError(f"{entry}: tensors of this kind are not supported")
+    _lib.check(out[0], entry)
+    return out[1:]
 
 
 def _option(table: dict, value: str, name: str) -> int:
@@ -110,51 +84,41 @@ def _option(table: dict, value: str, name: str) -> int:
     return table[value]
 
 
-def _policy(tokens, sequences, log_probs, old, advantages, ref, clip_low, clip_high, dual_clip,
-            kl_coef, kl_estimator, reduction, return_metrics, negated):
-    """(loss, grad, metrics or None) of flce_policy_loss on ``tokens``."""
-    shape, dtype, dev = log_probs.shape, log_probs.dtype, log_probs.device
-    estimator = _option(_lib.KL_ESTIMATORS, kl_estimator, "kl_estimator")
-    reduce = _option(_lib.TOKEN_REDUCTIONS, reduction, "reduction")
-    log_probs, ld = _laid_out(log_probs, shape, dtype, dev, "log_probs")
-    if advantages.dtype != torch.float32 or advantages.device != dev:
-        raise TypeError(f"advantages must be float32 on {dev}")
-    a_shape, ld_adv, per_token = advantages.shape, 0, 0
-    if a_shape == shape:
-        advantages, ld_adv = _laid_out(advantages, shape, torch.float32, dev, "advantages")
-        per_token = 1
-    elif a_shape == (sequences,) or a_shape == (sequences, 1):
+def _regular_policy(x, old, advantages, ref, mask, cu_seqlens, ignore_index):
+    lp, mask, cu = _regular_tokens(x, mask, cu_seqlens, ignore_index)
+    sequences = x.shape[0] if cu is None else cu.shape[0] - 1
+    if advantages.dtype != torch.float32 or advantages.device != x.device:
+        raise TypeError(f"advantages must be float32 on {x.device}")
+    if advantages.shape == x.shape:
+        advantages = _regular(advantages, x, torch.float32, "advantages")
+    elif advantages.shape == (sequences,) or advantages.shape == (sequences, 1):
         advantages = advantages.contiguous()
     else:
-        raise ValueError(f"advantages must be [{sequences}], one per sequence, or {tuple(shape)}, "
-                         f"one per token; got {tuple(a_shape)}")
-    old_at = ref_at = ld_old = ld_ref = 0
+        raise ValueError(f"advantages must be [{sequences}], one per sequence, or {tuple(x.shape)}, "
+                         f"one per token; got {tuple(advantages.shape)}")
     if old is not None:
-        old, ld_old = _laid_out(old, shape, dtype, dev, "old_log_probs")
-        old_at = old.data_ptr()
+        old = _regular(old, x, x.dtype, "old_log_probs")
     if ref is not None:
-        ref, ld_ref = _laid_out(ref, shape, dtype, dev, "ref_log_probs")
-        ref_at = ref.data_ptr()
-    elif kl_coef:
+        ref = _regular(ref, x, x.dtype, "ref_log_probs")
+    return lp, old, advantages, ref, mask, cu, ignore_index
+
+
+def _policy(log_probs, old, advantages, ref, mask, cu_seqlens, ignore_index, clip_low, clip_high,
+            dual_clip, kl_coef, kl_estimator, reduction, return_metrics, negated):
+    """(loss, grad), or (loss, grad, kl_sum, num_tokens, num_clipped), of flce_policy_loss.
+
+    With ``ignore_index`` the mask is int64 labels.
+    """
+    if kl_coef and ref is None:
         raise ValueError("kl_coef needs ref_log_probs")
-    grad = _float_like(log_probs, shape, dev)
-    ws_at = ws_bytes = 0
-    if grad.numel() > _SMALL or sequences > 1024:
-        ws = torch.empty(_POLICY_WORKSPACE + 8 * sequences, dtype=torch.uint8, device=dev)
-        ws_at, ws_bytes = ws.data_ptr(), ws.numel()
-    f0, i0 = _scalar_templates(dev)
-    loss, metrics, kl_at, n_at, clipped_at = torch.empty_like(f0), None, 0, 0, 0
-    if return_metrics:
-        kl_sum, n, clipped = torch.empty_like(f0), torch.empty_like(i0), torch.empty_like(i0)
-        kl_at, n_at, clipped_at = kl_sum.data_ptr(), n.data_ptr(), clipped.data_ptr()
-        metrics = {"num_tokens": n, "num_clipped": clipped, "kl_sum": kl_sum}
-    args = _lib.POLICY_ARGS.pack(
-        *tokens, log_probs.data_ptr(), old_at, ref_at, advantages.data_ptr(), loss.data_ptr(),
-        grad.data_ptr(), n_at, clipped_at, kl_at, ws_at, ws_bytes, ld, ld_old, ld_ref, ld_adv,
-        shape[-1], clip_low, clip_high, dual_clip or 0.0, kl_coef, _DTYPES[dtype], per_token,
-        estimator, reduce, negated, 0)
-    _lib.check(_lib.policy_loss_raw(args, _stream(dev)), "flce_policy_loss")
-    return loss, grad, metrics
+    return _call(_lib.tensors().policy, "flce_policy_loss", _regular_policy,
+                 (log_probs, old, advantages, ref, mask, cu_seqlens, ignore_index),
+                 (clip_low, clip_high, dual_clip or 0.0, kl_coef,
+                  _option(_lib.KL_ESTIMATORS, kl_estimator, "kl_estimator"),
+                  _option(_lib.TOKEN_REDUCTIONS, reduction, "reduction"), negated, return_metrics))
+
+
+_METRICS = ("kl_sum", "num_tokens", "num_clipped")
 
 
 def policy_loss_and_grad(log_probs: torch.Tensor, old_log_probs: Optional[torch.Tensor],
@@ -179,42 +143,29 @@ def policy_loss_and_grad(log_probs: torch.Tensor, old_log_probs: Optional[torch.
     Returns ``(loss, grad)``, both float32, or ``(loss, grad, metrics)`` with
     the device scalars num_tokens, num_clipped (int64) and kl_sum.
     """
-    tokens, sequences, keep = _tokens(log_probs, mask, cu_seqlens, "log_probs")
-    loss, grad, metrics = _policy(tokens, sequences, log_probs, old_log_probs, advantages,
-                                  ref_log_probs, clip_low, clip_high, dual_clip, kl_coef,
-                                  kl_estimator, reduction, return_metrics, 0)
-    return (loss, grad, metrics) if return_metrics else (loss, grad)
+    loss, grad, *metrics = _policy(log_probs, old_log_probs, advantages, ref_log_probs, mask, cu_seqlens,
+                                   None, clip_low, clip_high, dual_clip, kl_coef, kl_estimator,
+                                   reduction, return_metrics, 0)
+    return (loss, grad, dict(zip(_METRICS, metrics))) if return_metrics else (loss, grad)
 
 
-def _preference(tokens, sequences, log_probs, ref, beta, loss_type, label_smoothing, margin,
-                average, negated):
-    """(loss, grad, chosen rewards, rejected rewards) of flce_preference_loss on ``tokens``."""
-    if sequences % 2:
+def _regular_preference(x, ref, mask, cu_seqlens, ignore_index):
+    lp, mask, cu = _regular_tokens(x, mask, cu_seqlens, ignore_index)
+    if (x.shape[0] if cu is None else cu.shape[0] - 1) % 2:
         raise ValueError("a preference batch needs an even number of sequences: the chosen ones, "
                          "then the rejected ones")
-    shape, dtype, dev = log_probs.shape, log_probs.dtype, log_probs.device
-    kind = _option(_lib.PREFERENCE_LOSSES, loss_type, "loss_type")
-    log_probs, ld = _laid_out(log_probs, shape, dtype, dev, "log_probs")
-    ref_at = ld_ref = 0
     if ref is not None:
-        ref, ld_ref = _laid_out(ref, shape, dtype, dev, "ref_log_probs")
-        ref_at = ref.data_ptr()
-    pairs = sequences // 2
-    grad = _float_like(log_probs, shape, dev)
-    loss = torch.empty_like(_scalar_templates(dev)[0])
-    chosen = torch.empty(pairs, dtype=torch.float32, device=dev)
-    rejected = torch.empty_like(chosen)
+        ref = _regular(ref, x, x.dtype, "ref_log_probs")
+    return lp, ref, mask, cu, ignore_index
 
-    ws_at = ws_bytes = 0
-    if grad.numel() > _SMALL or pairs > 64:
-        ws = torch.empty(_PREFERENCE_WORKSPACE + 4 * pairs, dtype=torch.uint8, device=dev)
-        ws_at, ws_bytes = ws.data_ptr(), ws.numel()
-    args = _lib.PREFERENCE_ARGS.pack(
-        *tokens, log_probs.data_ptr(), ref_at, loss.data_ptr(), grad.data_ptr(), chosen.data_ptr(),
-        rejected.data_ptr(), ws_at, ws_bytes, ld, ld_ref, shape[-1], beta, label_smoothing, margin, _DTYPES[dtype], kind,
-        1 if average else 0, negated)
-    _lib.check(_lib.preference_loss_raw(args, _stream(dev)), "flce_preference_loss")
-    return loss, grad, chosen, rejected
+
+def _preference(log_probs, ref, mask, cu_seqlens, ignore_index, beta, loss_type, label_smoothing,
+                margin, average, negated):
+    """(loss, grad, chosen rewards, rejected rewards) of flce_preference_loss, as ``_policy``."""
+    return _call(_lib.tensors().preference, "flce_preference_loss", _regular_preference,
+                 (log_probs, ref, mask, cu_seqlens, ignore_index),
+                 (beta, label_smoothing, margin, _option(_lib.PREFERENCE_LOSSES, loss_type, "loss_type"),
+                  1 if average else 0, negated))
 
 
 def preference_loss_and_grad(log_probs: torch.Tensor, ref_log_probs: Optional[torch.Tensor] = None,
@@ -231,8 +182,7 @@ def preference_loss_and_grad(log_probs: torch.Tensor, ref_log_probs: Optional[to
     Returns ``(loss, grad, chosen_rewards, rejected_rewards)``, all float32;
     the rewards are beta times each sequence's log ratio.
     """
-    tokens, sequences, keep = _tokens(log_probs, mask, cu_seqlens, "log_probs")
-    return _preference(tokens, sequences, log_probs, ref_log_probs, beta, loss_type,
+    return _preference(log_probs, ref_log_probs, mask, cu_seqlens, None, beta, loss_type,
                        label_smoothing, margin, average, 0)
 
 
@@ -258,9 +208,6 @@ class _LogProbLoss(torch.autograd.Function):
     @staticmethod
     def backward(ctx, grad_loss, *_):
         return _scaled(ctx.saved_tensors[0], grad_loss).to(ctx.dtype), None
-
-
-_METRICS = ("num_tokens", "num_clipped", "kl_sum")
 
 
 def policy_loss(log_probs: torch.Tensor, old_log_probs: Optional[torch.Tensor],
@@ -329,11 +276,8 @@ def fused_linear_policy_loss(hidden: torch.Tensor, weight: torch.Tensor, targets
     gradients; the logits are never stored.
     """
     def fn(nll, labels):
-        tokens, sequences, keep = _label_tokens(nll, labels, ignore_index, cu_seqlens)
-        loss, grad, m = _policy(tokens, sequences, nll, old_log_probs, advantages, ref_log_probs,
-                                clip_low, clip_high, dual_clip, kl_coef, kl_estimator, reduction,
-                                True, 1)
-        return (loss, grad, *(m[k] for k in _METRICS))
+        return _policy(nll, old_log_probs, advantages, ref_log_probs, labels, cu_seqlens, ignore_index,
+                       clip_low, clip_high, dual_clip, kl_coef, kl_estimator, reduction, True, 1)
     loss, *m = _FusedLinear.apply(hidden, weight, bias, targets, (ignore_index, logit_scale, softcap),
                                   fn)
     return (loss, dict(zip(_METRICS, m))) if return_metrics else loss
@@ -354,7 +298,6 @@ def fused_linear_preference_loss(hidden: torch.Tensor, weight: torch.Tensor, tar
     rejected_rewards)``; hidden, weight and bias receive gradients.
     """
     def fn(nll, labels):
-        tokens, sequences, keep = _label_tokens(nll, labels, ignore_index, cu_seqlens)
-        return _preference(tokens, sequences, nll, ref_log_probs, beta, loss_type, label_smoothing,
-                           margin, average, 1)
+        return _preference(nll, ref_log_probs, labels, cu_seqlens, ignore_index, beta, loss_type,
+                           label_smoothing, margin, average, 1)
     return _FusedLinear.apply(hidden, weight, bias, targets, (ignore_index, logit_scale, softcap), fn)

@@ -76,3 +76,13 @@ def test_a_missing_build_is_refused(monkeypatch, tmp_path):
     monkeypatch.setattr(_lib, "TENSORS_PATH", str(tmp_path / "none.so"))
     with pytest.raises(RuntimeError, match="is missing"):
         _lib.tensors()
+
+
+def test_losses_leave_tensors_that_are_not_on_a_gpu_alone():
+    t, x = _lib.tensors(), torch.zeros(2, 3)
+    assert t.policy(0, 0, x, None, x, None, None, None, None, 0.2, 0.2, 0.0, 0.0, 2, 1, 0, 1) is None
+    assert t.preference(0, 0, x, None, None, None, None, 0.1, 0.0, 0.0, 0, 0, 0) is None
+    assert t.policy(0, 0, None, *[None] * 6, 0.2, 0.2, 0.0, 0.0, 2, 1, 0, 1) is None
+    for f in (t.policy, t.preference):
+        with pytest.raises(TypeError):
+            f(0, 0, x)

@@ -65,13 +65,17 @@ def _regular_tokens(x, mask, cu_seqlens, ignore_index):
     return _regular(x, x, x.dtype, "log_probs"), mask, cu_seqlens
 
 
-def _call(fn, entry: str, regular, tensors: tuple, numbers: tuple):
-    """The outputs of a call through flce_tensors, if need be on what ``regular`` makes of the tensors."""
-    x, at = tensors[0], _lib.entry_address(entry)
-    out = fn(at, _stream(x.device), *tensors, *numbers) if x.is_cuda else None
+def _call(name: str, regular, tensors: tuple, numbers: tuple):
+    """The outputs of flce_<name>_loss, if need be on what ``regular`` makes of the tensors."""
+    x = tensors[0]
+    if not x.is_cuda:
+        regular(*tensors)   # raises
+    fn, entry = getattr(_lib.tensors(), name), f"flce_{name}_loss"
+    at, stream = _lib.entry_address(entry), _stream(x.device)
+    out = fn(at, stream, *tensors, *numbers)
     if out is None:
         tensors = regular(*tensors)   # raises where something is wrong
-        out = fn(at, _stream(x.device), *tensors, *numbers)
+        out = fn(at, stream, *tensors, *numbers)
         if out is None:
             raise TypeError(f"{entry}: tensors of this kind are not supported")
     _lib.check(out[0], entry)
@@ -111,7 +115,7 @@ def _policy(log_probs, old, advantages, ref, mask, cu_seqlens, ignore_index, cli
     """
     if kl_coef and ref is None:
         raise ValueError("kl_coef needs ref_log_probs")
-    return _call(_lib.tensors().policy, "flce_policy_loss", _regular_policy,
+    return _call("policy", _regular_policy,
                  (log_probs, old, advantages, ref, mask, cu_seqlens, ignore_index),
                  (clip_low, clip_high, dual_clip or 0.0, kl_coef,
                   _option(_lib.KL_ESTIMATORS, kl_estimator, "kl_estimator"),
@@ -162,7 +166,7 @@ def _regular_preference(x, ref, mask, cu_seqlens, ignore_index):
 def _preference(log_probs, ref, mask, cu_seqlens, ignore_index, beta, loss_type, label_smoothing,
                 margin, average, negated):
     """(loss, grad, chosen rewards, rejected rewards) of flce_preference_loss, as ``_policy``."""
-    return _call(_lib.tensors().preference, "flce_preference_loss", _regular_preference,
+    return _call("preference", _regular_preference,
                  (log_probs, ref, mask, cu_seqlens, ignore_index),
                  (beta, label_smoothing, margin, _option(_lib.PREFERENCE_LOSSES, loss_type, "loss_type"),
                   1 if average else 0, negated))

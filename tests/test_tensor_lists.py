@@ -1,9 +1,18 @@
 """flce_tensors: what the AdamW step asks of lists of tensors, on CPU tensors."""
+import os
+
 import numpy as np
 import pytest
 import torch
 
 from linear_cross_entropy_tiled_gb300 import _lib
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    if not os.path.exists(_lib.TENSORS_PATH):
+        import __graft_entry__
+        __graft_entry__.build()
 
 
 def lists():
